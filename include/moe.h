@@ -1,6 +1,7 @@
 /*
  * moe.h -- C ABI of the B200 (sm_100a) DiT-MoE sparse expert layer: the
- * forward, the balance loss's statistics over ranks and its gradient.
+ * forward, the backward, the balance loss's statistics over ranks and over packed
+ * sequences with its gradients, and the optimizer's step.
  *
  * The layer (for every image-patch token x_t, width D):
  *   logits  l[t,i] = x_t . Wg[i] (+ b_i)                 i = 0..E-1
@@ -469,6 +470,78 @@ int moe_router_backward(const moe_config_t* cfg, const void* x, const void* wg, 
  */
 int moe_expert_frequency(const moe_config_t* cfg, const int32_t* topk_idx, const int32_t* n_sel, int32_t seq_len,
                          const int32_t* seq_labels, int32_t n_labels, int32_t* hist, void* ws, void* stream);
+
+/*
+ * The optimizer: AdamW over many tensors at once, with the gradient norm it clips by (the pages
+ * train the DiT-MoE models with AdamW and keep a moving average of the weights; "Scalable
+ * Diffusion Models with Transformers (DiT)", training settings).  At step t, with the gradient g
+ * times its factor:
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
+ *   param = param (1 - lr wd) - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ *   weight = param rounded to its type,   ema = ema_decay ema + (1 - ema_decay) param
+ * Moments are fp32, or 8-bit (MOE_MOMENTS_E4M3): 256 consecutive elements share one fp32 scale,
+ * the largest magnitude / 448, and a moment is scale times an e4m3 code; `v` then holds codes of
+ * sqrt(v).  Codes are rounded up or down at random, right on average, by bits hashed from (seed,
+ * step, place of the tensor in the list, element): equal calls give equal bits.  A block of 256
+ * whose largest moment is below 2^-100 or not finite is stored as zeros.
+ */
+typedef enum { MOE_MOMENTS_F32 = 0, MOE_MOMENTS_E4M3 = 1 } moe_moments_t;
+
+typedef struct {
+  float* param;          /* [n] fp32 master, updated */
+  const void* grad;      /* [n] of grad_dtype */
+  void* weight;          /* [n] of weight_dtype (bf16 or fp16): the rounded copy, written; or NULL */
+  void* m; void* v;      /* [n] moments, updated: fp32, or uint8 codes */
+  float* m_scale;        /* [ceil(n / 256)] scales of the 8-bit moments (NULL for fp32 moments) */
+  float* v_scale;
+  float* ema;            /* [n] fp32 moving average, updated; or NULL */
+  int64_t n;             /* elements, >= 0 (0: the pointers are not looked at) */
+  float weight_decay;
+  int32_t grad_dtype;    /* moe_dtype_t */
+  int32_t weight_dtype;  /* moe_dtype_t, read where weight is set */
+  int32_t reserved;      /* 0 */
+} moe_adamw_tensor_t;
+
+typedef struct {
+  double lr, beta1, beta2, eps;
+  double ema_decay;      /* in [0, 1]; read where a tensor has an average */
+  double grad_mult;      /* factor of every gradient when clipped = 0 (1 / loss scale, say) */
+  uint64_t seed;         /* of the 8-bit moments' rounding */
+  int32_t state;         /* moe_moments_t */
+  int32_t clipped;       /* 1: use the factor that the last moe_grad_norm on `ctl` left, and leave everything
+                            as it is where it found a gradient that is not finite */
+} moe_adamw_t;
+
+/*
+ * moe_optim_init -- set up `ctl`, the optimizer's 256-byte control block on the device (256-byte
+ * aligned), with `step` steps taken:
+ *   bytes 0 int64 steps taken; 8, 16 fp64 beta1^step, beta2^step; 24 fp32 factor of lr (1: a
+ *   program writes it to change the rate under a captured graph); 28 fp32 gradient norm; 32 fp32
+ *   factor of the gradients; 36 int32 1 = a gradient was not finite; 40 int64 steps skipped for
+ *   that; 48, 52 counters, zero between launches.
+ * Calls that share a ctl run one after another.
+ */
+int moe_optim_init(void* ctl, int64_t step, double beta1, double beta2, void* stream);
+
+/*
+ * moe_grad_norm -- grad_mult times the 2-norm of every tensor's gradient together (the fields grad,
+ * n and grad_dtype; the others are not read), into ctl: the norm, the factor of the gradients
+ * grad_mult min(1, max_norm / (norm + 1e-6)) (grad_mult where max_norm is 0), and whether one was
+ * not finite (the factor is then 0).  Squares are summed in fp64 in a fixed order.
+ *   ws   scratch of moe_grad_norm_workspace_size(n_tensors) bytes, 256-byte aligned
+ * One launch for up to 1100 tensors.
+ */
+size_t moe_grad_norm_workspace_size(int32_t n_tensors);
+int moe_grad_norm(const moe_adamw_tensor_t* tensors, int32_t n_tensors, double grad_mult, double max_norm, void* ctl,
+                  void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * moe_adamw_step -- one step of every tensor (see above), which ctl then counts.  The list and the
+ * settings are host memory, read before the call returns.  Tensors must not overlap.  One launch
+ * for up to 340 tensors; no scratch.  A captured call replays as the next step.
+ */
+int moe_adamw_step(const moe_adamw_t* settings, const moe_adamw_tensor_t* tensors, int32_t n_tensors, void* ctl,
+                   void* stream);
 
 #ifdef __cplusplus
 }

@@ -523,3 +523,46 @@ def canonical_permutation(idx, E, tile=128):
             row_slot[r] = k
     return {"counts": counts, "offsets": offsets, "padded_offsets": padded,
             "pos": pos, "row_token": row_token, "row_slot": row_slot}
+
+
+# ---------------------------------------------------------------- optimizer
+
+def grad_norm(grads, grad_mult=1.0, max_norm=0.0):
+    """(norm, factor): grad_mult times the 2-norm of all gradients together, and the factor that
+    brings them to max_norm at most (grad_mult alone where max_norm is 0)."""
+    norm = grad_mult * math.sqrt(sum(float(np.sum(as_f64(g) ** 2)) for g in grads))
+    return norm, grad_mult * (min(1.0, max_norm / (norm + 1e-6)) if max_norm > 0 else 1.0)
+
+
+def adamw(p, g, m, v, t, lr, betas, eps, wd):
+    """Step t of AdamW ("Scalable Diffusion Models with Transformers (DiT)", training settings: AdamW):
+    the new (p, m, v) with decoupled weight decay wd and bias-corrected moments."""
+    p, g, m, v = as_f64(p), as_f64(g), as_f64(m), as_f64(v)
+    m = betas[0] * m + (1 - betas[0]) * g
+    v = betas[1] * v + (1 - betas[1]) * g * g
+    mh, vh = m / (1 - betas[0] ** t), v / (1 - betas[1] ** t)
+    return p - lr * wd * p - lr * mh / (np.sqrt(vh) + eps), m, v
+
+
+def rounding_bits(seed, step, tensor, n):
+    """The 32 random bits of each of a tensor's n elements in one step (the 8-bit moments' rounding):
+    a 64-bit key of (seed, step, tensor), then twice a 32 x 32 -> 64 bit product, folded, of the
+    element's place.  The odd multipliers are the fractions of 1/phi and of sqrt(2) and sqrt(3)."""
+    m64, m32 = (1 << 64) - 1, np.uint64(0xFFFFFFFF)
+    h = (seed + step * 0x9E3779B97F4A7C15 + tensor * 0xBB67AE8584CAA73B) & m64
+    h = ((h ^ (h >> 29)) * 0x6A09E667F3BCC909) & m64
+    key = (h ^ (h >> 32)) >> 1
+    s = np.uint64(32)
+    z = ((np.arange(n, dtype=np.uint64) + np.uint64(key & 0xFFFFFFFF)) & m32) * np.uint64(0x9E3779B9)
+    z = ((z & m32) ^ (z >> s) ^ np.uint64(key >> 32)) * np.uint64(0x6A09E667)
+    return ((z & m32) ^ (z >> s)).astype(np.uint32)
+
+
+def e4m3_round(a, r16):
+    """Magnitudes a in [0, 448] rounded to a neighbouring e4m3 value: up where the part above the lower
+    neighbour, in units of the gap, and the 16 random bits over 2^16 make one together.  Returns the
+    value and how far that sum is from the nearest whole number of gaps."""
+    a = as_f64(a)
+    gap = 2.0 ** (np.floor(np.log2(np.maximum(a, 2.0 ** -6))) - 3)
+    q = a / gap + np.asarray(r16, dtype=F64) / 65536
+    return np.minimum(np.floor(q) * gap, 448.0), np.abs(q - np.rint(q))

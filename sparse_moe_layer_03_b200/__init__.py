@@ -1,14 +1,14 @@
-"""B200-native DiT-MoE sparse expert layer (forward, with the balance loss's
-statistics and gradient): C-ABI library + thin binding.
+"""B200-native DiT-MoE sparse expert layer (forward, backward, the balance loss's
+statistics and gradients, the optimizer's step): C-ABI library + thin binding.
 
 ``inputs`` (seeded synthetic workloads) and ``metrics`` (work accounting) load
 without a GPU.  The compute entry points live in ``binding`` (ctypes over
-``libmoe.so``) and ``layer`` (buffer management around the four calls); they
-load the CUDA library on import and fail loudly when it is missing.
+``libmoe.so``), ``layer`` (buffer management around the four calls) and ``optim``
+(gradient norm and AdamW); they load the CUDA library on import and fail loudly when it is missing.
 """
 import importlib
 
-__all__ = ["inputs", "metrics", "binding", "layer"]
+__all__ = ["inputs", "metrics", "binding", "layer", "optim"]
 
 
 def __getattr__(name):

@@ -19,6 +19,7 @@ MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE = 0, -1, -2,
 MOE_ERR_CUDA, MOE_ERR_DEVICE_CHECK, MOE_ERR_TIMEOUT = -4, -5, -6
 MOE_F32, MOE_BF16, MOE_F16 = 0, 1, 2
 MOE_ROUTE_TOPK, MOE_ROUTE_RACE = 0, 1
+MOE_MOMENTS_F32, MOE_MOMENTS_E4M3 = 0, 1
 MOE_GEMM_AUTO, MOE_GEMM_SIMT, MOE_GEMM_TC1 = 0, 1, 2
 
 
@@ -72,6 +73,17 @@ def make_expert_grads(dw1, db1, dw2, db2, dws1, dbs1, dws2, dbs2):
     return MoeExpertGrads(*[_ptr(t) for t in (dw1, db1, dw2, db2, dws1, dbs1, dws2, dbs2)])
 
 
+class MoeAdamwTensor(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("param", "grad", "weight", "m", "v", "m_scale", "v_scale", "ema")] + [
+        ("n", C.c_int64), ("weight_decay", C.c_float), ("grad_dtype", C.c_int32), ("weight_dtype", C.c_int32),
+        ("reserved", C.c_int32)]
+
+
+class MoeAdamw(C.Structure):
+    _fields_ = [(n, C.c_double) for n in ("lr", "beta1", "beta2", "eps", "ema_decay", "grad_mult")] + [
+        ("seed", C.c_uint64), ("state", C.c_int32), ("clipped", C.c_int32)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"moe error {code}: {msg}")
@@ -114,6 +126,10 @@ _SIGS = {
                                       _P, C.POINTER(MoeExpertGrads), _P, _P, _P, C.c_size_t, _P, C.c_size_t, _P]),
     "moe_router_backward": (C.c_int, [_CFG, _P, _P, _P, _P, _P, _P, _P, C.c_float, _P, _P, _P, C.c_int32, _P,
                                       C.c_size_t, _P]),
+    "moe_optim_init": (C.c_int, [_P, C.c_int64, C.c_double, C.c_double, _P]),
+    "moe_grad_norm_workspace_size": (C.c_size_t, [C.c_int32]),
+    "moe_grad_norm": (C.c_int, [C.POINTER(MoeAdamwTensor), C.c_int32, C.c_double, C.c_double, _P, _P, C.c_size_t, _P]),
+    "moe_adamw_step": (C.c_int, [C.POINTER(MoeAdamw), C.POINTER(MoeAdamwTensor), C.c_int32, _P, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(lib, _name)
@@ -290,3 +306,25 @@ def moe_router_backward(cfg, x, wg, router_bias, counts, topk_idx, n_sel, dgate,
     _check(lib.moe_router_backward(C.byref(cfg), _ptr(x), _ptr(wg), _ptr(router_bias), _ptr(counts), _ptr(topk_idx),
                                    _ptr(n_sel), _ptr(dgate), aux_scale, _ptr(dwg), _ptr(dbias), _ptr(dx),
                                    int(dx_accumulate), _ptr(bws), bws_bytes, stream))
+
+
+def moe_optim_init(ctl, step, beta1, beta2, stream=0):
+    """Set up the optimizer's 256-byte control block with ``step`` steps taken."""
+    _check(lib.moe_optim_init(_ptr(ctl), step, beta1, beta2, stream))
+
+
+def moe_grad_norm_workspace_size(n_tensors) -> int:
+    n = lib.moe_grad_norm_workspace_size(n_tensors)
+    if n == 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, lib.moe_last_error().decode())
+    return n
+
+
+def moe_grad_norm(tensors, n_tensors, grad_mult, max_norm, ctl, ws, ws_bytes, stream=0):
+    """Norm of all gradients, the clip factor and the not-finite flag, into the control block."""
+    _check(lib.moe_grad_norm(tensors, n_tensors, grad_mult, max_norm, _ptr(ctl), _ptr(ws), ws_bytes, stream))
+
+
+def moe_adamw_step(settings, tensors, n_tensors, ctl, stream=0):
+    """One AdamW step of ``tensors`` (a ctypes array of MoeAdamwTensor) with ``settings`` (MoeAdamw)."""
+    _check(lib.moe_adamw_step(C.byref(settings), tensors, n_tensors, _ptr(ctl), stream))

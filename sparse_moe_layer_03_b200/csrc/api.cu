@@ -6,6 +6,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -1118,6 +1119,98 @@ int moe_combine(const moe_config_t* cfg, const void* y_perm, const void* y_sh,
   cudaError_t e = launch_combine(ca, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "combine kernel");
   return ok();
+}
+
+// ---------------------------------------------------------------- optimizer
+static int check_ctl(const void* ctl) {
+  if (!ctl) return fail(MOE_ERR_INVALID_ARG, "ctl is NULL");
+  if ((uintptr_t)ctl & 255u) return fail(MOE_ERR_INVALID_ARG, "ctl must be 256-byte aligned");
+  return MOE_OK;
+}
+static int check_grads(const moe_adamw_tensor_t* t, int32_t n) {
+  if (n < 0) return fail(MOE_ERR_INVALID_ARG, "n_tensors=%d < 0", n);
+  if (n > 0 && !t) return fail(MOE_ERR_INVALID_ARG, "tensors is NULL");
+  long long sum = 0;
+  for (int i = 0; i < n; ++i) {
+    if (t[i].n < 0) return fail(MOE_ERR_INVALID_ARG, "tensor %d: n=%lld < 0", i, (long long)t[i].n);
+    if (t[i].n > (1ll << 40)) return fail(MOE_ERR_UNSUPPORTED, "tensor %d: n=%lld above 2^40", i, (long long)t[i].n);
+    sum += (t[i].n + 2047) / 2048;
+    if (t[i].n == 0) continue;
+    if (!t[i].grad || !aligned16(t[i].grad))
+      return fail(MOE_ERR_INVALID_ARG, "tensor %d: grad is NULL or not 16-byte aligned", i);
+    if (t[i].grad_dtype != MOE_F32 && t[i].grad_dtype != MOE_BF16 && t[i].grad_dtype != MOE_F16)
+      return fail(MOE_ERR_INVALID_ARG, "tensor %d: grad_dtype=%d", i, t[i].grad_dtype);
+  }
+  if (sum > 0x7fffffffll) return fail(MOE_ERR_UNSUPPORTED, "above 2^42 elements in one call");
+  return MOE_OK;
+}
+
+int moe_optim_init(void* ctl, int64_t step, double beta1, double beta2, void* stream) {
+  int rc = check_ctl(ctl);
+  if (rc) return rc;
+  if (step < 0) return fail(MOE_ERR_INVALID_ARG, "step=%lld < 0", (long long)step);
+  if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0))
+    return fail(MOE_ERR_INVALID_ARG, "beta1=%g or beta2=%g outside [0, 1)", beta1, beta2);
+  const cudaError_t e = launch_optim_init(static_cast<OptCtl*>(ctl), step, pow(beta1, (double)step),
+                                          pow(beta2, (double)step), (cudaStream_t)stream);
+  return e == cudaSuccess ? ok() : cuda_fail(e, "moe_optim_init");
+}
+
+size_t moe_grad_norm_workspace_size(int32_t n_tensors) {
+  if (n_tensors < 0) {
+    fail(MOE_ERR_INVALID_ARG, "n_tensors=%d < 0", n_tensors);
+    return 0;
+  }
+  return round_up(grad_norm_scratch(n_tensors), 256);
+}
+
+int moe_grad_norm(const moe_adamw_tensor_t* tensors, int32_t n_tensors, double grad_mult, double max_norm, void* ctl,
+                  void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_grads(tensors, n_tensors);
+  if (rc || (rc = check_ctl(ctl))) return rc;
+  if (!(grad_mult > 0.0) || !std::isfinite(grad_mult)) return fail(MOE_ERR_INVALID_ARG, "grad_mult=%g", grad_mult);
+  if (!(max_norm >= 0.0)) return fail(MOE_ERR_INVALID_ARG, "max_norm=%g < 0", max_norm);
+  if (!ws) return fail(MOE_ERR_INVALID_ARG, "ws is NULL");
+  if ((uintptr_t)ws & 255u) return fail(MOE_ERR_INVALID_ARG, "ws must be 256-byte aligned");
+  const size_t need = moe_grad_norm_workspace_size(n_tensors);
+  if (ws_bytes < need) return fail(MOE_ERR_WORKSPACE, "ws_bytes=%zu < %zu", ws_bytes, need);
+  const cudaError_t e = launch_grad_norm(tensors, n_tensors, grad_mult, max_norm, static_cast<OptCtl*>(ctl),
+                                         static_cast<double*>(ws), num_sms_current(), (cudaStream_t)stream);
+  return e == cudaSuccess ? ok() : cuda_fail(e, "gradient norm");
+}
+
+int moe_adamw_step(const moe_adamw_t* settings, const moe_adamw_tensor_t* tensors, int32_t n_tensors, void* ctl,
+                   void* stream) {
+  if (!settings) return fail(MOE_ERR_INVALID_ARG, "settings is NULL");
+  const moe_adamw_t& h = *settings;
+  int rc = check_grads(tensors, n_tensors);
+  if (rc || (rc = check_ctl(ctl))) return rc;
+  if (h.state != MOE_MOMENTS_F32 && h.state != MOE_MOMENTS_E4M3) return fail(MOE_ERR_INVALID_ARG, "state=%d", h.state);
+  if (!(h.beta1 >= 0.0 && h.beta1 < 1.0) || !(h.beta2 >= 0.0 && h.beta2 < 1.0))
+    return fail(MOE_ERR_INVALID_ARG, "beta1=%g or beta2=%g outside [0, 1)", h.beta1, h.beta2);
+  if (!std::isfinite(h.lr) || !(h.eps >= 0.0) || !std::isfinite(h.eps))
+    return fail(MOE_ERR_INVALID_ARG, "lr=%g or eps=%g", h.lr, h.eps);
+  if (!h.clipped && !std::isfinite(h.grad_mult)) return fail(MOE_ERR_INVALID_ARG, "grad_mult=%g", h.grad_mult);
+  for (int i = 0; i < n_tensors; ++i) {
+    const moe_adamw_tensor_t& t = tensors[i];
+    if (t.n == 0) continue;
+    const void* need[] = {t.param, t.m, t.v};
+    for (const void* p : need)
+      if (!p || !aligned16(p))
+        return fail(MOE_ERR_INVALID_ARG, "tensor %d: param, m or v is NULL or not 16-byte aligned", i);
+    if (h.state == MOE_MOMENTS_E4M3 && (!t.m_scale || !t.v_scale))
+      return fail(MOE_ERR_INVALID_ARG, "tensor %d: 8-bit moments need m_scale and v_scale", i);
+    if (!aligned16(t.weight) || !aligned16(t.ema) || ((uintptr_t)t.m_scale & 3u) || ((uintptr_t)t.v_scale & 3u))
+      return fail(MOE_ERR_INVALID_ARG, "tensor %d: weight or ema is not 16-byte aligned, or a scale not 4-byte", i);
+    if (t.weight && t.weight_dtype != MOE_BF16 && t.weight_dtype != MOE_F16)
+      return fail(MOE_ERR_INVALID_ARG, "tensor %d: weight_dtype=%d (bf16 or fp16)", i, t.weight_dtype);
+    if (!std::isfinite(t.weight_decay)) return fail(MOE_ERR_INVALID_ARG, "tensor %d: weight_decay", i);
+    if (t.ema && !(h.ema_decay >= 0.0 && h.ema_decay <= 1.0))
+      return fail(MOE_ERR_INVALID_ARG, "ema_decay=%g outside [0, 1]", h.ema_decay);
+  }
+  const cudaError_t e = launch_adamw(h, tensors, n_tensors, static_cast<OptCtl*>(ctl), num_sms_current(),
+                                     (cudaStream_t)stream);
+  return e == cudaSuccess ? ok() : cuda_fail(e, "AdamW step");
 }
 
 }  // extern "C"

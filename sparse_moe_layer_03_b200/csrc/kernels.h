@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "../../include/moe.h"
+
 namespace moe {
 
 // message returned by moe_last_error() on this thread
@@ -274,5 +276,22 @@ struct CombineArgs {
   int img_len;
 };
 cudaError_t launch_combine(const CombineArgs& a, cudaStream_t s);
+
+// ---- optim.cu: gradient norm and AdamW over many tensors
+// The optimizer's control block on the device (the layout of moe.h's moe_optim_init).
+struct OptCtl {
+  long long step;            // steps taken
+  double beta1_t, beta2_t;   // beta1^step, beta2^step
+  float lr_scale;
+  float grad_norm, grad_scale;
+  int nonfinite;
+  long long skipped;
+  unsigned int norm_done, step_done;   // blocks done, zero between launches
+};
+size_t grad_norm_scratch(int n);
+cudaError_t launch_optim_init(OptCtl* c, long long step, double b1t, double b2t, cudaStream_t s);
+cudaError_t launch_grad_norm(const moe_adamw_tensor_t* t, int n, double mult, double max_norm, OptCtl* ctl, double* parts,
+                             int sms, cudaStream_t s);
+cudaError_t launch_adamw(const moe_adamw_t& h, const moe_adamw_tensor_t* t, int n, OptCtl* ctl, int sms, cudaStream_t s);
 
 }  // namespace moe

@@ -273,6 +273,12 @@ class MoELayer:
                               self.stream())
         return g
 
+    def optimizer(self, **settings) -> "LayerAdamW":  # noqa: F821
+        """AdamW of this layer's weights (``optim.LayerAdamW``): ``opt.step(layer.backward(x, dout))``
+        rewrites them in place."""
+        from .optim import LayerAdamW
+        return LayerAdamW(self, **settings)
+
     # ------------------------------------------------------------ serving from host memory
     def forward_host_pipelined(self, x_host, out_host, aux_host=None):
         """Run the layer over a sequence of host batches, overlapping transfers with compute.

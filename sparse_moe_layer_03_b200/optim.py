@@ -1,0 +1,235 @@
+"""The optimizer of a training step on one GPU: gradient norm, clipping and AdamW.
+
+Buffers and argument checks around ``moe_grad_norm`` and ``moe_adamw_step``; the
+arithmetic is in the library's kernels.  Every call runs on the current CUDA stream of
+the tensors' device, reads nothing back, and can be captured in a CUDA graph (the step
+count lives on the device: a replay is the next step).
+
+    opt = layer.optimizer(lr=1e-4, state="e4m3", ema_decay=0.9999)   # masters from the layer's weights
+    out = layer.forward(x)
+    opt.step(layer.backward(x, dout), max_norm=1.0)                  # the layer's weights are the new ones
+"""
+from __future__ import annotations
+
+from typing import Optional, Sequence
+
+import torch
+
+from . import binding as B
+
+BLOCK = 256            # elements that share a scale of 8-bit moments; each tensor's state starts on such a block
+_DTYPE = {torch.float32: B.MOE_F32, torch.bfloat16: B.MOE_BF16, torch.float16: B.MOE_F16}
+
+
+def _stream(device) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _check(t, what, dtypes, device, n=None):
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
+        raise ValueError(f"{what} must be a tensor of {' or '.join(str(d) for d in dtypes)}")
+    if t.device != device:
+        raise ValueError(f"{what} is on {t.device}, not on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{what} has {t.numel()} elements, not {n}")
+
+
+class _Control:
+    """The 256-byte control block on the device and views of its words."""
+
+    def __init__(self, device):
+        self.device = torch.device(device)
+        if self.device.type == "cuda" and self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        self.ctl = torch.zeros(256, dtype=torch.uint8, device=self.device)
+        self._step = self.ctl[0:8].view(torch.int64)
+        self.lr_scale = self.ctl[24:28].view(torch.float32)      # factor of lr; write it between replays of a graph
+        self.grad_norm = self.ctl[28:32].view(torch.float32)     # of the last norm: [1] tensors on the device
+        self.grad_scale = self.ctl[32:36].view(torch.float32)
+        self.nonfinite = self.ctl[36:40].view(torch.int32)
+        self.skipped = self.ctl[40:48].view(torch.int64)         # steps that a non-finite gradient left out
+        self._ws = None
+
+    def _init(self, step, betas):
+        with torch.cuda.device(self.device):
+            B.moe_optim_init(self.ctl, step, betas[0], betas[1], _stream(self.device))
+
+    def _norm(self, tensors, n, max_norm, grad_mult):
+        need = B.moe_grad_norm_workspace_size(n)
+        if self._ws is None or self._ws.numel() < need:
+            self._ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+        B.moe_grad_norm(tensors, n, grad_mult, max_norm, self.ctl, self._ws, self._ws.numel(), _stream(self.device))
+
+
+def _fill_grads(tensors, grads, device, sizes=None):
+    for i, (t, g) in enumerate(zip(tensors, grads)):
+        if g is None:
+            t.n = 0                                  # no gradient: the tensor stays as it is
+            continue
+        _check(g, f"grads[{i}]", tuple(_DTYPE), device, None if sizes is None else sizes[i])
+        t.grad, t.n, t.grad_dtype = g.data_ptr(), g.numel(), _DTYPE[g.dtype]
+
+
+class GradNorm(_Control):
+    """2-norm of a list of gradients (fp32, bf16 or fp16) together, and the factor that clips them.
+
+    ``norm, scale = GradNorm(device)(grads, max_norm=1.0)``: views of the control block, [1] fp32 each,
+    overwritten by the next call.  ``scale`` is 0 and ``nonfinite`` 1 where a gradient is not finite."""
+
+    def __init__(self, device="cuda:0"):
+        super().__init__(device)
+        self._init(0, (0.0, 0.0))
+        self._tensors = None
+
+    def __call__(self, grads: Sequence[Optional[torch.Tensor]], max_norm: float = 0.0, grad_mult: float = 1.0):
+        n = len(grads)
+        if self._tensors is None or len(self._tensors) != n:
+            self._tensors = (B.MoeAdamwTensor * n)()
+        _fill_grads(self._tensors, grads, self.device)
+        with torch.cuda.device(self.device):
+            self._norm(self._tensors, n, max_norm, grad_mult)
+        return self.grad_norm, self.grad_scale
+
+
+class AdamW(_Control):
+    """AdamW over many tensors in one launch.
+
+    ``params``: fp32 tensors, updated in place.  ``weights``: for each its bf16 or fp16 copy, which
+    every step rewrites, or None.  ``weight_decay``: one value or one for each tensor.  ``state``:
+    "f32" moments, or "e4m3" ones (8 bits, 256 elements to a scale, rounded at random by ``seed``).
+    ``ema_decay``: keep a moving average of the params.  ``buffers`` holds the state: one flat tensor
+    of each kind ("m", "v", "m_scale", "v_scale", "ema"; "v" holds sqrt(v) for "e4m3"), in which
+    ``params[i]``'s part starts at element ``starts[i]``, a multiple of 256 (of 1 in the scales).
+    """
+
+    def __init__(self, params: Sequence[torch.Tensor], weights: Optional[Sequence[Optional[torch.Tensor]]] = None, *,
+                 lr: float, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay=0.0, state: str = "f32",
+                 ema_decay: Optional[float] = None, seed: int = 0):
+        params = list(params)
+        if not params or not isinstance(params[0], torch.Tensor) or params[0].device.type != "cuda":
+            raise ValueError("params must be a list of CUDA tensors")
+        super().__init__(params[0].device)
+        weights = [None] * len(params) if weights is None else list(weights)
+        decay = [float(weight_decay)] * len(params) if isinstance(weight_decay, (int, float)) else list(weight_decay)
+        if len(weights) != len(params) or len(decay) != len(params):
+            raise ValueError("weights and weight_decay need one entry for each tensor")
+        if state not in ("f32", "e4m3"):
+            raise ValueError(f"state={state!r}: 'f32' or 'e4m3'")
+        if not (0.0 <= betas[0] < 1.0 and 0.0 <= betas[1] < 1.0):
+            raise ValueError(f"betas={betas} outside [0, 1)")
+        spans = []
+        for i, (p, w) in enumerate(zip(params, weights)):
+            _check(p, f"params[{i}]", (torch.float32,), self.device)
+            spans.append((p.data_ptr(), p.numel() * 4, f"params[{i}]"))
+            if w is not None:
+                _check(w, f"weights[{i}]", (torch.bfloat16, torch.float16), self.device, p.numel())
+                spans.append((w.data_ptr(), w.numel() * 2, f"weights[{i}]"))
+        spans = sorted(s for s in spans if s[1])
+        for a, b in zip(spans, spans[1:]):
+            if a[0] + a[1] > b[0]:
+                raise ValueError(f"{a[2]} and {b[2]} overlap")
+        self.params, self.weights, self.betas = params, weights, (float(betas[0]), float(betas[1]))
+        self.sizes = [p.numel() for p in params]
+        self.starts, total = [], 0
+        for n in self.sizes:
+            self.starts.append(total)
+            total += -(-n // BLOCK) * BLOCK
+        z = lambda n, dt: torch.zeros(n, dtype=dt, device=self.device)  # noqa: E731
+        q8 = state == "e4m3"
+        self.buffers = {k: z(total, torch.float8_e4m3fn if q8 else torch.float32) for k in ("m", "v")}
+        if q8:
+            self.buffers.update({k: z(total // BLOCK, torch.float32) for k in ("m_scale", "v_scale")})
+        if ema_decay is not None:
+            self.buffers["ema"] = z(total, torch.float32)
+            for p, at in zip(params, self.starts):
+                self.buffers["ema"][at:at + p.numel()].copy_(p.reshape(-1))
+        self.settings = B.MoeAdamw(lr, self.betas[0], self.betas[1], eps, 0.0 if ema_decay is None else ema_decay, 1.0,
+                                   seed % (1 << 64), B.MOE_MOMENTS_E4M3 if q8 else B.MOE_MOMENTS_F32, 0)
+        self._tensors = (B.MoeAdamwTensor * len(params))()
+        at = {k: b.data_ptr() for k, b in self.buffers.items()}
+        for t, p, w, wd, s in zip(self._tensors, params, weights, decay, self.starts):
+            t.param, t.weight_decay = p.data_ptr(), wd
+            if w is not None:
+                t.weight, t.weight_dtype = w.data_ptr(), _DTYPE[w.dtype]
+            size = 1 if q8 else 4
+            t.m, t.v = at["m"] + s * size, at["v"] + s * size
+            if q8:
+                t.m_scale, t.v_scale = (at[k] + s // BLOCK * 4 for k in ("m_scale", "v_scale"))
+            if ema_decay is not None:
+                t.ema = at["ema"] + s * 4
+        self._init(0, self.betas)
+
+    @property
+    def lr(self) -> float:
+        return self.settings.lr
+
+    @lr.setter
+    def lr(self, v: float):
+        self.settings.lr = v                         # a captured graph keeps its own: scale that by lr_scale
+
+    def steps_taken(self) -> int:
+        """Steps taken so far (waits for the device)."""
+        return int(self._step.item())
+
+    def part(self, name: str, i: int) -> torch.Tensor:
+        """Tensor i's part of ``buffers[name]``."""
+        per = BLOCK if name.endswith("_scale") else 1
+        at = self.starts[i] // per
+        return self.buffers[name][at:at + -(-self.sizes[i] // per)]
+
+    def step(self, grads: Sequence[Optional[torch.Tensor]], max_norm: Optional[float] = None, grad_mult: float = 1.0):
+        """One step.  ``grads``: fp32, bf16 or fp16, one for each tensor (None leaves a tensor as it is),
+        taken times ``grad_mult``.  With ``max_norm`` the norm over all of them is formed first
+        (``grad_norm``), they are clipped to it (0: not clipped), and a gradient that is not finite
+        leaves everything as it is and counts in ``skipped``."""
+        if len(grads) != len(self.params):
+            raise ValueError(f"{len(grads)} gradients for {len(self.params)} tensors")
+        _fill_grads(self._tensors, grads, self.device, self.sizes)
+        n = len(self.params)
+        with torch.cuda.device(self.device):
+            if max_norm is not None:
+                self._norm(self._tensors, n, max_norm, grad_mult)
+            self.settings.clipped = int(max_norm is not None)
+            self.settings.grad_mult = grad_mult
+            B.moe_adamw_step(self.settings, self._tensors, n, self.ctl, _stream(self.device))
+
+    def state_dict(self) -> dict:
+        """Copies of the state and the step count (waits for the device)."""
+        return dict({k: b.clone() for k, b in self.buffers.items()}, step=self.steps_taken())
+
+    def load_state_dict(self, state: dict):
+        if set(state) != set(self.buffers) | {"step"}:
+            raise ValueError(f"state has {sorted(state)}, not {sorted(self.buffers) + ['step']}")
+        for k, b in self.buffers.items():
+            if state[k].shape != b.shape or state[k].dtype != b.dtype:
+                raise ValueError(f"state[{k!r}] is {tuple(state[k].shape)} {state[k].dtype}, not {tuple(b.shape)} {b.dtype}")
+        for k, b in self.buffers.items():
+            b.copy_(state[k])
+        self._init(int(state["step"]), self.betas)
+
+
+class LayerAdamW(AdamW):
+    """AdamW of a ``MoELayer``'s weights: fp32 masters made from them (an fp32 weight is its own), the
+    layer's tensors rewritten by every step.  ``weight_decay`` (one value) is for the matrices; biases
+    have none.  ``step`` takes what ``MoELayer.backward`` returns."""
+
+    NAMES = (("wg", "dwg"), ("w1", "dw1"), ("w2", "dw2"), ("ws1", "dws1"), ("ws2", "dws2"),
+             ("router_bias", "dbias"), ("b1", "db1"), ("b2", "db2"), ("bs1", "dbs1"), ("bs2", "dbs2"))
+
+    def __init__(self, layer, *, weight_decay: float = 0.0, **settings):
+        self.grad_names, params, weights, decay = [], [], [], []
+        for name, grad in self.NAMES:
+            w = getattr(layer, name)
+            if w is None:
+                continue
+            own = w.dtype == torch.float32
+            self.grad_names.append(grad)
+            params.append(w if own else w.float())
+            weights.append(None if own else w)
+            decay.append(0.0 if "b" in name else weight_decay)
+        super().__init__(params, weights, weight_decay=decay, **settings)
+
+    def step(self, grads: dict, max_norm: Optional[float] = None, grad_mult: float = 1.0):
+        super().step([grads[n] for n in self.grad_names], max_norm, grad_mult)
