@@ -472,6 +472,37 @@ int moe_expert_frequency(const moe_config_t* cfg, const int32_t* topk_idx, const
                          const int32_t* seq_labels, int32_t n_labels, int32_t* hist, void* ws, void* stream);
 
 /*
+ * moe_seq_balance -- the expert-level balance loss of each packed sequence ("MOE-DIT", eq.
+ * L_balance with T the length of one image-patch sequence), its per-expert counts and, joined
+ * with the gates' gradient, its gradient through the router: moe_balance_loss_backward and
+ * moe_router_backward for a loss per image, over images of one or of many lengths.
+ *   loss_b = alpha sum_i (E/(K L_b)) seq_counts[b,i] (1/L_b) sum_{t in b} P[t,i]
+ *   loss   = the mean of loss_b over the sequences that hold a row (0 if none does)
+ *   dJ/dP  = aux_scale dloss/dP + dgate on the selected slots
+ *   x, wg, router_bias   as given to moe_route (the scores are recomputed in fp32)
+ *   seq_offsets [n_seqs+1] int32 ascending, 0..T: sequence b is rows seq_offsets[b] ..
+ *               seq_offsets[b+1]-1 and may be empty.  NULL: images of cfg->seq_len rows each (0: the
+ *               whole call is one), n_seqs = T / seq_len.  Rows of no sequence take no part: their
+ *               x may hold anything and their rows of dx stay as they are.
+ *   topk_idx, n_sel      from moe_route (n_sel NULL: K slots for every token)
+ *   dgate       [T,Kmax] fp32 from moe_expert_backward, or NULL
+ *   aux_scale   dJ/dloss
+ *   seq_counts  [n_seqs,E] int32 out: selected pairs of each sequence and expert
+ *   seq_loss    [n_seqs] fp32 out; loss [1] fp32 out
+ *   dwg         [E,D] fp32 out, or NULL for the loss and the counts alone (then dbias and dx too)
+ *   dbias       [E] fp32 out or NULL; dx [T,D] act out or NULL; dx_accumulate 1: dx += the router's part
+ *   bws         scratch of moe_seq_balance_workspace_size(cfg, n_seqs) bytes, 256-byte aligned
+ *   ws          status word only: offsets that descend or leave 0..T, or an expert id >= E (which is
+ *               skipped), are reported through moe_check_status
+ * Every type; fixed-order sums, bit-reproducible.
+ */
+size_t moe_seq_balance_workspace_size(const moe_config_t* cfg, int32_t n_seqs);
+int moe_seq_balance(const moe_config_t* cfg, const void* x, const void* wg, const float* router_bias,
+                    const int32_t* seq_offsets, int32_t n_seqs, const int32_t* topk_idx, const int32_t* n_sel,
+                    const float* dgate, float aux_scale, int32_t* seq_counts, float* seq_loss, float* loss, float* dwg,
+                    float* dbias, void* dx, int32_t dx_accumulate, void* bws, size_t bws_bytes, void* ws, void* stream);
+
+/*
  * The optimizer: AdamW over many tensors at once, with the gradient norm it clips by (the pages
  * train the DiT-MoE models with AdamW and keep a moving average of the weights; "Scalable
  * Diffusion Models with Transformers (DiT)", training settings).  At step t, with the gradient g

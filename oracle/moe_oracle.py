@@ -566,3 +566,30 @@ def e4m3_round(a, r16):
     gap = 2.0 ** (np.floor(np.log2(np.maximum(a, 2.0 ** -6))) - 3)
     q = a / gap + np.asarray(r16, dtype=F64) / 65536
     return np.minimum(np.floor(q) * gap, 448.0), np.abs(q - np.rint(q))
+
+
+# ---------------------------------------------------------------- balance loss over packed sequences
+
+def balance_packed(idx, P, K, alpha, offsets):
+    """L_balance of each packed sequence ("MOE-DIT", eq. L_balance, T the length of the sequence), rows
+    offsets[b] .. offsets[b+1]-1: (mean over the sequences that hold a row, the losses, the counts
+    [n, E], dL/dP of the mean [T, E]).  Rows of no sequence have no part in any of them."""
+    P = as_f64(P)
+    T, E = P.shape
+    idx = np.asarray(idx).reshape(T, -1)
+    n = len(offsets) - 1
+    losses, counts, dP = np.zeros(n), np.zeros((n, E), dtype=np.int64), np.zeros((T, E))
+    full = sum(1 for b in range(n) if offsets[b + 1] > offsets[b])
+    for b in range(n):
+        rows = slice(int(offsets[b]), int(offsets[b + 1]))
+        L = rows.stop - rows.start
+        if L > 0:
+            counts[b] = expert_counts(idx[rows], E)
+            losses[b] = balance_loss(counts[b], P[rows], K, alpha)
+            dP[rows] = alpha * (E / (K * L)) * counts[b] / L / full
+    return float(losses.sum() / max(full, 1)), losses, counts, dP
+
+
+def softmax_backward(P, dP):
+    """dl = P (dP - sum_j P dP)."""
+    return P * (dP - np.sum(P * dP, axis=1, keepdims=True))

@@ -126,6 +126,9 @@ _SIGS = {
                                       _P, C.POINTER(MoeExpertGrads), _P, _P, _P, C.c_size_t, _P, C.c_size_t, _P]),
     "moe_router_backward": (C.c_int, [_CFG, _P, _P, _P, _P, _P, _P, _P, C.c_float, _P, _P, _P, C.c_int32, _P,
                                       C.c_size_t, _P]),
+    "moe_seq_balance_workspace_size": (C.c_size_t, [_CFG, C.c_int32]),
+    "moe_seq_balance": (C.c_int, [_CFG, _P, _P, _P, _P, C.c_int32, _P, _P, _P, C.c_float, _P, _P, _P, _P, _P, _P,
+                                  C.c_int32, _P, C.c_size_t, _P, _P]),
     "moe_optim_init": (C.c_int, [_P, C.c_int64, C.c_double, C.c_double, _P]),
     "moe_grad_norm_workspace_size": (C.c_size_t, [C.c_int32]),
     "moe_grad_norm": (C.c_int, [C.POINTER(MoeAdamwTensor), C.c_int32, C.c_double, C.c_double, _P, _P, C.c_size_t, _P]),
@@ -306,6 +309,22 @@ def moe_router_backward(cfg, x, wg, router_bias, counts, topk_idx, n_sel, dgate,
     _check(lib.moe_router_backward(C.byref(cfg), _ptr(x), _ptr(wg), _ptr(router_bias), _ptr(counts), _ptr(topk_idx),
                                    _ptr(n_sel), _ptr(dgate), aux_scale, _ptr(dwg), _ptr(dbias), _ptr(dx),
                                    int(dx_accumulate), _ptr(bws), bws_bytes, stream))
+
+
+def moe_seq_balance_workspace_size(cfg, n_seqs) -> int:
+    n = lib.moe_seq_balance_workspace_size(C.byref(cfg), n_seqs)
+    if n == 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, lib.moe_last_error().decode())
+    return n
+
+
+def moe_seq_balance(cfg, x, wg, router_bias, seq_offsets, n_seqs, topk_idx, n_sel, dgate, aux_scale, seq_counts, seq_loss,
+                    loss, dwg, dbias, dx, dx_accumulate, bws, bws_bytes, ws, stream=0):
+    """Balance loss per packed sequence, its counts and (dwg given) its and the gates' gradient through the router."""
+    _check(lib.moe_seq_balance(C.byref(cfg), _ptr(x), _ptr(wg), _ptr(router_bias), _ptr(seq_offsets), n_seqs,
+                               _ptr(topk_idx), _ptr(n_sel), _ptr(dgate), aux_scale, _ptr(seq_counts), _ptr(seq_loss),
+                               _ptr(loss), _ptr(dwg), _ptr(dbias), _ptr(dx), dx_accumulate, _ptr(bws), bws_bytes, _ptr(ws),
+                               stream))
 
 
 def moe_optim_init(ctl, step, beta1, beta2, stream=0):

@@ -1121,6 +1121,102 @@ int moe_combine(const moe_config_t* cfg, const void* y_perm, const void* y_sh,
   return ok();
 }
 
+// ---------------------------------------------------------------- balance loss over packed sequences
+struct SbLayout { size_t live, tok, tok_loss, frag, scales, dl, db_part, partials, total; };
+static SbLayout sb_layout(const moe_config_t* c) {
+  SbLayout L{};
+  const size_t T = (size_t)c->T, nblk = (T + 15) / 16, ep = (size_t)seq_balance_ep(c->E);
+  int ranges = 0, per = 0;
+  seq_balance_plan(c->T, c->D, c->dtype, &ranges, &per);
+  size_t off = 0;
+  auto take = [&](size_t bytes) { size_t o = off; off += round_up(bytes ? bytes : 1, 256); return o; };
+  L.live = take(256);
+  L.tok = take(T * 8);
+  L.tok_loss = take(T * 4);
+  L.frag = take(is16(c) ? nblk * 1024 * (ep / 8) : 0);
+  L.scales = take(c->dtype == MOE_F16 ? nblk * kSbScales * 4 : 0);
+  L.dl = take(is16(c) ? 0 : T * ep * 4);
+  L.db_part = take(nblk * ep * 4);
+  L.partials = take((size_t)ranges * c->E * c->D * 4);
+  L.total = off;
+  return L;
+}
+static int check_seqs(const moe_config_t* c, int32_t n_seqs) {
+  int rc = validate(c);
+  if (rc) return rc;
+  if (n_seqs < 0) return fail(MOE_ERR_INVALID_ARG, "n_seqs=%d < 0", n_seqs);
+  if (n_seqs > kMaxT) return fail(MOE_ERR_UNSUPPORTED, "n_seqs=%d above the supported %d", n_seqs, kMaxT);
+  return MOE_OK;
+}
+
+size_t moe_seq_balance_workspace_size(const moe_config_t* cfg, int32_t n_seqs) {
+  return check_seqs(cfg, n_seqs) == MOE_OK ? sb_layout(cfg).total : 0;
+}
+
+int moe_seq_balance(const moe_config_t* cfg, const void* x, const void* wg, const float* router_bias,
+                    const int32_t* seq_offsets, int32_t n_seqs, const int32_t* topk_idx, const int32_t* n_sel,
+                    const float* dgate, float aux_scale, int32_t* seq_counts, float* seq_loss, float* loss, float* dwg,
+                    float* dbias, void* dx, int32_t dx_accumulate, void* bws, size_t bws_bytes, void* ws, void* stream) {
+  int rc = check_seqs(cfg, n_seqs);
+  if (rc) return rc;
+  const int seq_len = cfg->seq_len > 0 ? cfg->seq_len : cfg->T;
+  if (!seq_offsets && (long long)n_seqs * seq_len != cfg->T)
+    return fail(MOE_ERR_INVALID_ARG, "n_seqs=%d images of %d tokens are not T=%d", n_seqs, seq_len, cfg->T);
+  if (!dwg && (dbias || dx || dgate)) return fail(MOE_ERR_INVALID_ARG, "dbias, dx and dgate need dwg");
+  if (dx_accumulate && !dx) return fail(MOE_ERR_INVALID_ARG, "dx_accumulate needs dx");
+  if (!std::isfinite(aux_scale)) return fail(MOE_ERR_INVALID_ARG, "aux_scale=%g", aux_scale);
+  if (cfg->routing == MOE_ROUTE_RACE && !n_sel) return fail(MOE_ERR_INVALID_ARG, "n_sel is required for Expert-Race routing");
+  if (n_seqs > 0) {
+    REQUIRE_PTR(seq_counts);
+    REQUIRE_PTR(seq_loss);
+  }
+  if (!loss) return fail(MOE_ERR_INVALID_ARG, "loss is NULL");
+  OPTIONAL_PTR(dwg);
+  OPTIONAL_PTR(dbias);
+  if (!bws) return fail(MOE_ERR_INVALID_ARG, "bws is NULL");
+  if ((uintptr_t)bws & 255u) return fail(MOE_ERR_INVALID_ARG, "bws must be 256-byte aligned");
+  const SbLayout L = sb_layout(cfg);
+  if (bws_bytes < L.total) return fail(MOE_ERR_WORKSPACE, "bws_bytes=%zu < %zu", bws_bytes, L.total);
+  if (!ws) return fail(MOE_ERR_INVALID_ARG, "ws is NULL");
+  cudaStream_t s = (cudaStream_t)stream;
+  cudaError_t e;
+  if (cfg->T == 0) {
+    struct { void* p; size_t n; } z[] = {{seq_counts, (size_t)n_seqs * cfg->E * 4}, {seq_loss, (size_t)n_seqs * 4}, {loss, 4},
+                                         {dwg, (size_t)cfg->E * cfg->D * 4}, {dbias, (size_t)cfg->E * 4}};
+    for (auto& q : z)
+      if (q.p && q.n && (e = cudaMemsetAsync(q.p, 0, q.n, s)) != cudaSuccess) return cuda_fail(e, "moe_seq_balance");
+    return ok();
+  }
+  REQUIRE_PTR(x);
+  REQUIRE_PTR(wg);
+  REQUIRE_PTR(topk_idx);
+  OPTIONAL_PTR(router_bias);
+  OPTIONAL_PTR(seq_offsets);
+  OPTIONAL_PTR(n_sel);
+  OPTIONAL_PTR(dgate);
+  OPTIONAL_PTR(dx);
+  SeqBalArgs a{};
+  a.x = x; a.wg = wg; a.bias = router_bias;
+  a.T = cfg->T; a.D = cfg->D; a.E = cfg->E; a.K = cfg->K; a.Kmax = kmax_of(cfg); a.dtype = cfg->dtype;
+  a.alpha = cfg->alpha; a.aux_scale = aux_scale;
+  a.offsets = seq_offsets; a.n_seqs = n_seqs; a.seq_len = seq_len;
+  a.topk_idx = topk_idx; a.n_sel = n_sel; a.dgate = dgate;
+  a.counts = seq_counts; a.seq_loss = seq_loss; a.loss = loss;
+  a.grads = dwg != nullptr; a.dwg = dwg; a.dbias = dbias; a.dx = dx; a.accumulate = dx_accumulate != 0;
+  seq_balance_plan(cfg->T, cfg->D, cfg->dtype, &a.ranges, &a.blocks_per_range);
+  a.live = ws_at<int>(bws, L.live);
+  a.tok = ws_at<int2>(bws, L.tok);
+  a.tok_loss = ws_at<float>(bws, L.tok_loss);
+  a.frag = ws_at<uint4>(bws, L.frag);
+  a.scales = ws_at<float>(bws, L.scales);
+  a.dl = ws_at<float>(bws, L.dl);
+  a.db_part = ws_at<float>(bws, L.db_part);
+  a.partials = ws_at<float>(bws, L.partials);
+  a.status = status_ptr(ws);
+  if ((e = launch_seq_balance(a, s)) != cudaSuccess) return cuda_fail(e, "balance loss over sequences");
+  return ok();
+}
+
 // ---------------------------------------------------------------- optimizer
 static int check_ctl(const void* ctl) {
   if (!ctl) return fail(MOE_ERR_INVALID_ARG, "ctl is NULL");

@@ -277,6 +277,35 @@ struct CombineArgs {
 };
 cudaError_t launch_combine(const CombineArgs& a, cudaStream_t s);
 
+// ---- seq_balance.cu: the balance loss over packed sequences, with its gradient
+struct SeqBalArgs {
+  const void* x; const void* wg; const float* bias;   // x [T,D], wg [E,D] act; bias [E] or null
+  int T, D, E, K, Kmax, dtype;
+  float alpha, aux_scale;
+  const int32_t* offsets; int n_seqs, seq_len;        // [n_seqs + 1] row borders, or null: seq_len rows each
+  const int32_t* topk_idx; const int32_t* n_sel;      // n_sel null: K slots each
+  const float* dgate;                                 // [T,Kmax] or null
+  int32_t* counts; float* seq_loss; float* loss;      // outputs [n_seqs,E], [n_seqs], [1]
+  int grads;                                          // the gradients below are wanted
+  float* dwg; float* dbias; void* dx; int accumulate; // dbias and dx may be null
+  int ranges, blocks_per_range;                       // seq_balance_plan
+  // scratch
+  int2* tok;                                          // [T] sequence (-1: none) and factor of its counts
+  int* live;                                          // [1] sequences with a row
+  float* tok_loss;                                    // [T]
+  uint4* frag;                                        // 16-bit: dl in fragment order, 1 KB a block and 8 experts
+  float* scales;                                      // fp16: [blocks, kSbScales] inverse scales of the fragments
+  float* dl;                                          // fp32: [T, ep]
+  float* db_part;                                     // [blocks, ep]
+  float* partials;                                    // [ranges, E, D]
+  int* status;
+};
+constexpr int kSbScales = 20;                         // 16 rows, then the block
+constexpr int kSbJobs = 148 * 16;                     // warps of the gradient kernel: one wave
+int seq_balance_ep(int E);                            // experts rounded up to 8, 16 or 32
+void seq_balance_plan(int T, int D, int dtype, int* ranges, int* blocks_per_range);
+cudaError_t launch_seq_balance(const SeqBalArgs& a, cudaStream_t s);
+
 // ---- optim.cu: gradient norm and AdamW over many tensors
 // The optimizer's control block on the device (the layout of moe.h's moe_optim_init).
 struct OptCtl {

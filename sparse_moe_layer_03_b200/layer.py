@@ -239,13 +239,48 @@ class MoELayer:
         B.moe_check_status(self.ws, self.stream())
 
     # ------------------------------------------------------------ backward
-    def backward(self, x: torch.Tensor, dout: torch.Tensor, aux_scale: float = 1.0) -> dict:
+    def seq_balance(self, x: torch.Tensor, seq_offsets: Optional[torch.Tensor] = None,
+                    dgate: Optional[torch.Tensor] = None, aux_scale: float = 1.0, grads: Optional[dict] = None) -> dict:
+        """The last routing's balance loss per packed sequence: ``balance_loss`` [1] (the mean over the
+        sequences that hold a token), ``seq_loss`` [n] and ``seq_counts`` [n, E].
+
+        ``seq_offsets`` [n + 1] (int32, on the device): sequence b is rows seq_offsets[b] ..
+        seq_offsets[b+1]-1 of ``x``; rows of no sequence take no part.  Without it, images of the shape's
+        ``seq_len`` tokens.  ``grads`` (a dict with dwg, dbias, dx) receives the router's gradients of
+        aux_scale * balance_loss, with those of the gates ``dgate``; its dx is added to."""
+        s, dev = self.s, self.device
+        if seq_offsets is None:
+            n = self.cfg.T // s.seq_len if s.seq_len else min(self.cfg.T, 1)
+        else:
+            if seq_offsets.dtype != torch.int32 or seq_offsets.dim() != 1 or seq_offsets.numel() < 1 \
+                    or seq_offsets.device != x.device or not seq_offsets.is_contiguous():
+                raise ValueError("seq_offsets must be a contiguous int32 tensor [n + 1] on the layer's device")
+            n = seq_offsets.numel() - 1
+        nb = B.moe_seq_balance_workspace_size(self.cfg, n)
+        if getattr(self, "_sbws", None) is None or self._sbws.numel() < nb:
+            self._sbws = torch.empty(nb, dtype=torch.uint8, device=dev)
+        out = {"seq_counts": torch.empty((n, s.E), dtype=torch.int32, device=dev),
+               "seq_loss": torch.empty((n,), dtype=torch.float32, device=dev),
+               "balance_loss": torch.empty((1,), dtype=torch.float32, device=dev)}
+        g = grads or {}
+        B.moe_seq_balance(self.cfg, x, self.wg, self.router_bias, seq_offsets, n, self.topk_idx, self.n_sel, dgate,
+                          aux_scale, out["seq_counts"], out["seq_loss"], out["balance_loss"], g.get("dwg"),
+                          g.get("dbias"), g.get("dx"), int("dx" in g), self._sbws, self._sbws.numel(), self.ws,
+                          self.stream())
+        return out
+
+    def backward(self, x: torch.Tensor, dout: torch.Tensor, aux_scale: float = 1.0,
+                 seq_offsets: Optional[torch.Tensor] = None) -> dict:
         """Gradients of J = <dout, MoE(x)> + aux_scale * L_balance after ``forward(x)``.
 
         Returns fp32 gradients of every weight and bias (dw1, db1, dw2, db2, dws1, dbs1, dws2,
         dbs2, dwg, dbias), the gates' gradient ``dgate`` [T, Kmax] and ``dx`` (act dtype).  The
         selection is the forward's (discrete, no gradient).  Needs the forward's x_perm (the
-        default dispatch, not the gathered GEMM1)."""
+        default dispatch, not the gathered GEMM1).
+
+        With the shape's ``seq_len``, or ``seq_offsets`` [n + 1] (see ``seq_balance``), L_balance is the
+        mean over sequences, and ``balance_loss``, ``seq_loss`` and ``seq_counts`` are returned too; the
+        gates of rows that belong to no sequence then carry no gradient to the router."""
         if self.x_perm is None:
             raise ValueError("the backward reads x_perm: run the forward without gather_rows")
         s, dev, T = self.s, self.device, self.cfg.T
@@ -268,6 +303,9 @@ class MoELayer:
         B.moe_expert_backward(self.cfg, x, self.x_perm, self.offsets, self.pos, self.topk_idx, self.n_sel,
                               self.row_token, self.row_gate, wts, self.h_perm, self.h_sh, dout, grads, g["dgate"],
                               g["dx"], self.ws, self.ws_bytes, self._ebws, self._ebws_bytes, self.stream())
+        if s.seq_len or seq_offsets is not None:
+            g.update(self.seq_balance(x, seq_offsets, g["dgate"], aux_scale, g))
+            return g
         B.moe_router_backward(self.cfg, x, self.wg, self.router_bias, self.counts, self.topk_idx, self.n_sel,
                               g["dgate"], aux_scale, g["dwg"], g["dbias"], g["dx"], 1, self._rbws, self._rbws_bytes,
                               self.stream())
