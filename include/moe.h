@@ -514,7 +514,8 @@ int moe_seq_balance(const moe_config_t* cfg, const void* x, const void* wg, cons
  * the largest magnitude / 448, and a moment is scale times an e4m3 code; `v` then holds codes of
  * sqrt(v).  Codes are rounded up or down at random, right on average, by bits hashed from (seed,
  * step, place of the tensor in the list, element): equal calls give equal bits.  A block of 256
- * whose largest moment is below 2^-100 or not finite is stored as zeros.
+ * whose largest moment is below 2^-100 or not finite is stored as zeros.  The denominator is at
+ * least 2^-126 (eps = 0 with no gradient at all leaves a parameter as it is).
  */
 typedef enum { MOE_MOMENTS_F32 = 0, MOE_MOMENTS_E4M3 = 1 } moe_moments_t;
 

@@ -1122,22 +1122,23 @@ int moe_combine(const moe_config_t* cfg, const void* y_perm, const void* y_sh,
 }
 
 // ---------------------------------------------------------------- balance loss over packed sequences
-struct SbLayout { size_t live, tok, tok_loss, frag, scales, dl, db_part, partials, total; };
+struct SbLayout { size_t live, tok, tok_loss, blk_loss, frag, scales, dl, db_part, partials, total; };
 static SbLayout sb_layout(const moe_config_t* c) {
   SbLayout L{};
   const size_t T = (size_t)c->T, nblk = (T + 15) / 16, ep = (size_t)seq_balance_ep(c->E);
-  int ranges = 0, per = 0;
-  seq_balance_plan(c->T, c->D, c->dtype, &ranges, &per);
+  int groups = 0, per = 0;
+  seq_balance_plan(c->T, c->D, c->E, c->dtype, &groups, &per);
   size_t off = 0;
   auto take = [&](size_t bytes) { size_t o = off; off += round_up(bytes ? bytes : 1, 256); return o; };
   L.live = take(256);
   L.tok = take(T * 8);
   L.tok_loss = take(T * 4);
-  L.frag = take(is16(c) ? nblk * 1024 * (ep / 8) : 0);
-  L.scales = take(c->dtype == MOE_F16 ? nblk * kSbScales * 4 : 0);
+  L.blk_loss = take(is16(c) ? nblk * 4 : 0);
+  L.frag = take(is16(c) ? nblk * seq_balance_frag_bytes(c->E, c->dtype) : 0);
+  L.scales = take(c->dtype == MOE_F16 ? nblk * 128 : 0);
   L.dl = take(is16(c) ? 0 : T * ep * 4);
-  L.db_part = take(nblk * ep * 4);
-  L.partials = take((size_t)ranges * c->E * c->D * 4);
+  L.db_part = take(is16(c) ? nblk * ep * 4 : 0);
+  L.partials = take((size_t)groups * c->E * c->D * 4);
   L.total = off;
   return L;
 }
@@ -1203,12 +1204,13 @@ int moe_seq_balance(const moe_config_t* cfg, const void* x, const void* wg, cons
   a.topk_idx = topk_idx; a.n_sel = n_sel; a.dgate = dgate;
   a.counts = seq_counts; a.seq_loss = seq_loss; a.loss = loss;
   a.grads = dwg != nullptr; a.dwg = dwg; a.dbias = dbias; a.dx = dx; a.accumulate = dx_accumulate != 0;
-  seq_balance_plan(cfg->T, cfg->D, cfg->dtype, &a.ranges, &a.blocks_per_range);
+  seq_balance_plan(cfg->T, cfg->D, cfg->E, cfg->dtype, &a.groups, &a.blocks_per_range);
   a.live = ws_at<int>(bws, L.live);
   a.tok = ws_at<int2>(bws, L.tok);
   a.tok_loss = ws_at<float>(bws, L.tok_loss);
+  a.blk_loss = is16(cfg) ? ws_at<float>(bws, L.blk_loss) : nullptr;
   a.frag = ws_at<uint4>(bws, L.frag);
-  a.scales = ws_at<float>(bws, L.scales);
+  a.scales = ws_at<float4>(bws, L.scales);
   a.dl = ws_at<float>(bws, L.dl);
   a.db_part = ws_at<float>(bws, L.db_part);
   a.partials = ws_at<float>(bws, L.partials);

@@ -288,22 +288,24 @@ struct SeqBalArgs {
   int32_t* counts; float* seq_loss; float* loss;      // outputs [n_seqs,E], [n_seqs], [1]
   int grads;                                          // the gradients below are wanted
   float* dwg; float* dbias; void* dx; int accumulate; // dbias and dx may be null
-  int ranges, blocks_per_range;                       // seq_balance_plan
+  int groups, blocks_per_range;                       // seq_balance_plan
   // scratch
   int2* tok;                                          // [T] sequence (-1: none) and factor of its counts
   int* live;                                          // [1] sequences with a row
   float* tok_loss;                                    // [T]
-  uint4* frag;                                        // 16-bit: dl in fragment order, 1 KB a block and 8 experts
-  float* scales;                                      // fp16: [blocks, kSbScales] inverse scales of the fragments
+  float* blk_loss;                                    // 16-bit: [blocks] sums of 16 of them, else null
+  uint4* frag;                                        // 16-bit: dl in fragment order, seq_balance_frag_bytes a block
+  float4* scales;                                     // fp16: [blocks, 8] inverse scales of rows g, g + 8 and the block
   float* dl;                                          // fp32: [T, ep]
-  float* db_part;                                     // [blocks, ep]
-  float* partials;                                    // [ranges, E, D]
+  float* db_part;                                     // 16-bit: [blocks, ep]
+  float* partials;                                    // [groups, E, D]
   int* status;
 };
-constexpr int kSbScales = 20;                         // 16 rows, then the block
-constexpr int kSbJobs = 148 * 16;                     // warps of the gradient kernel: one wave
+constexpr int kSbSms = 148;                           // the plan (and so the sums' order) is one for every device
+constexpr int kSbF32Single = 148 * 32;                // fp32: tokens up to which a warp takes one at a time
 int seq_balance_ep(int E);                            // experts rounded up to 8, 16 or 32
-void seq_balance_plan(int T, int D, int dtype, int* ranges, int* blocks_per_range);
+size_t seq_balance_frag_bytes(int E, int dtype);
+void seq_balance_plan(int T, int D, int E, int dtype, int* groups, int* blocks_per_range);
 cudaError_t launch_seq_balance(const SeqBalArgs& a, cudaStream_t s);
 
 // ---- optim.cu: gradient norm and AdamW over many tensors

@@ -21,9 +21,11 @@
 // other state, and repeats bit for bit.
 //
 // One block is 256 threads on a chunk of 2048 elements; a warp owns 256 of them,
-// four consecutive ones in each lane and then four again 128 further on, so that
-// every 32-bit stream moves in 512-byte pieces and a warp's elements are exactly
-// one scale's.
+// eight consecutive ones in each lane, so that a warp's elements are exactly one
+// scale's and every fp32 stream moves in 32-byte vectors (two of 16 bytes where a
+// tensor is aligned to no more).
+#include <cuda_fp8.h>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -33,6 +35,7 @@ namespace {
 
 constexpr int kOptThreads = 256;
 constexpr int kOptChunk = kOptThreads * 8;         // elements of a block's chunk
+constexpr int kOptPerSm = 4;                       // resident blocks: 64 registers a thread
 constexpr int kScaleBlock = 256;                   // elements that share a scale
 constexpr int kNormChunk = kOptThreads * 16;
 constexpr int kOptSmall = 40, kOptLarge = 340;     // tensors a launch's parameters hold: under 4 KB, under 32 KB
@@ -50,21 +53,34 @@ __device__ __forceinline__ int find_tensor(const int* chunk_end, int n, int chun
   return lo;
 }
 
-// ---------------------------------------------------------------- gradient loads
-__device__ __forceinline__ void load4(const void* g, int dtype, long long i, float* f) {
-  if (dtype == 0) {
-    const float4 v = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(g) + i));
-    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+// ---------------------------------------------------------------- vectors of eight elements
+__device__ __forceinline__ void ld8(const float* p, bool wide, float* f) {
+  if (wide) {
+    asm volatile("ld.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
+                 : "l"(p));
   } else {
-    const uint2 v = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(g) + i));
-    if (dtype == 1) {
-      f[0] = __uint_as_float(v.x << 16); f[1] = __uint_as_float(v.x & 0xffff0000u);
-      f[2] = __uint_as_float(v.y << 16); f[3] = __uint_as_float(v.y & 0xffff0000u);
-    } else {
-      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&v.x));
-      const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
-      f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
-    }
+    const float4 u = *reinterpret_cast<const float4*>(p), v = *(reinterpret_cast<const float4*>(p) + 1);
+    f[0] = u.x; f[1] = u.y; f[2] = u.z; f[3] = u.w; f[4] = v.x; f[5] = v.y; f[6] = v.z; f[7] = v.w;
+  }
+}
+__device__ __forceinline__ void st8(float* p, bool wide, const float* f) {
+  if (wide) {
+    asm volatile("st.global.v8.f32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};"
+                 :: "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]), "l"(p)
+                 : "memory");
+  } else {
+    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    *(reinterpret_cast<float4*>(p) + 1) = make_float4(f[4], f[5], f[6], f[7]);
+  }
+}
+__device__ __forceinline__ void ld8_grad(const void* g, int dtype, long long i, bool wide, float* f) {
+  if (dtype == 0) {
+    ld8(static_cast<const float*>(g) + i, wide, f);
+  } else {
+    const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g) + i);
+    if (dtype == 1) bf16x8_to_f32(v, f);
+    else f16x8_to_f32(v, f);
   }
 }
 __device__ __forceinline__ float load1(const void* g, int dtype, long long i) {
@@ -79,7 +95,7 @@ struct NormParams {
   const void* g[CAP];
   long long n[CAP];
   int chunk_end[CAP];
-  uint8_t dtype[CAP];
+  uint8_t dtype[CAP], wide[CAP];   // wide: 32-byte aligned
   int tensors, chunks;
   int part0, nparts;       // this launch's first partial; partials of all launches (last launch only)
   int last;
@@ -116,7 +132,7 @@ __global__ void __launch_bounds__(kOptThreads) grad_norm_kernel(const __grid_con
     if (base + kNormChunk <= n) {
       float f[16];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) load4(g, dt, base + u * (kOptThreads * 4) + threadIdx.x * 4, f + 4 * u);
+      for (int u = 0; u < 2; ++u) ld8_grad(g, dt, base + u * (kOptThreads * 8) + threadIdx.x * 8, a.wide[k], f + 8 * u);
       double c[4] = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll
       for (int u = 0; u < 16; ++u) c[u & 3] = fma((double)f[u], (double)f[u], c[u & 3]);
@@ -163,6 +179,7 @@ struct OptTensor {
   float wd;
   int index;               // place in the call's list: keys the rounding
   uint8_t gdt, wdt;
+  uint8_t wide;            // every fp32 stream is 32-byte aligned
 };
 template <int CAP>
 struct AdamwParams {
@@ -192,43 +209,54 @@ __device__ __forceinline__ unsigned long long tensor_key(unsigned long long seed
   return (h ^ (h >> 32)) >> 1;
 }
 // 32 random bits for an element: twice a 32 x 32 -> 64 bit product, folded.
-__device__ __forceinline__ uint32_t element_bits(uint32_t i, uint32_t key_lo, uint32_t key_hi) {
-  unsigned long long z = (unsigned long long)(i + key_lo) * 0x9E3779B9u;
+__device__ __forceinline__ uint32_t element_bits(uint32_t i_plus_key_lo, uint32_t key_hi) {
+  unsigned long long z = (unsigned long long)i_plus_key_lo * 0x9E3779B9u;
   z = (unsigned long long)((uint32_t)z ^ (uint32_t)(z >> 32) ^ key_hi) * 0x6A09E667u;
   return (uint32_t)z ^ (uint32_t)(z >> 32);
 }
 
-// |x| <= 448 (a rounding above) to an e4m3 code: the fp32 bits below the code's three mantissa bits,
-// plus 16 random ones at their top, carry into the code with the probability that they are worth.
-// Below 2^-6 the codes are 2^-9 apart: adding 2^-6 gives the value that spacing.
-__device__ __forceinline__ uint32_t e4m3_code(float x, uint32_t r16) {
-  const float a = fabsf(x);
-  const bool low = a < 0.015625f;
-  const uint32_t bits = __float_as_uint(low ? a + 0.015625f : a) + (r16 << 4);
-  int code = (int)(bits >> 20) - (low ? 968 : 960);
-  code = code < 126 ? code : 126;
-  return (uint32_t)code | (x < 0.f ? 128u : 0u);
+// |x| <= 448 (a rounding or two above) to the code of a neighbouring e4m3 value, in the top byte.
+// Times 2^-120 the e4m3 exponents are fp32's own and e4m3's subnormals fp32's, so that bits 26..20
+// are the code of the value below in magnitude.  16 random bits under them carry with the probability
+// that the rest is worth, into subnormals and binades alike; their own four zero bits below leave
+// room for a rounding above 448.
+__device__ __forceinline__ uint32_t e4m3_random(float x, uint32_t r16_shl8) {
+  return (__float_as_uint(__fmul_rn(x, 0x1p-120f)) << 4) + r16_shl8;   // the sign is shifted out
 }
-// an e4m3 code's value: its exponent and mantissa moved to fp16's place (8 below in exponent), exactly
-__device__ __forceinline__ float e4m3_value(uint32_t code) {
-  const uint16_t h = (uint16_t)(((code & 0x80u) << 8) | ((code & 0x7fu) << 7));
-  return __half2float(__ushort_as_half(h)) * 256.f;
+__device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
+}
+__device__ __forceinline__ float2 e4m3_values(uint32_t codes) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
+  return __half22float2(__half2(h));
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 
-// m, v and the update in the same roundings as their formulas written out (no contraction), so that
-// the moments do not depend on how a compiler fuses them.  The update's quotient may be off by two
-// units: it is then scaled by lr and added to a parameter some thousand times larger.
+// m, v and the root in the roundings of their formulas written out (no contraction, IEEE square
+// root): what is kept does not depend on how a compiler fuses them.  The update's quotient goes
+// through an approximate reciprocal (one unit in the last place): it is then scaled by lr and added
+// to a parameter some thousand times larger.  A denominator below 2^-126 counts as that.
 __device__ __forceinline__ float moments(float g, float& m, float& v, const StepScalars& s) {
   m = __fadd_rn(__fmul_rn(s.b1, m), __fmul_rn(s.omb1, g));
   v = __fadd_rn(__fmul_rn(s.b2, v), __fmul_rn(s.omb2, __fmul_rn(g, g)));
   return __fsqrt_rn(v);
 }
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 __device__ __forceinline__ float update(float p, float m, float root, float keep, const StepScalars& s) {
-  return fmaf(-s.step_size, __fdividef(m, fmaf(root, s.rs2, s.eps)), __fmul_rn(p, keep));
+  const float den = max_nan(fmaf(root, s.rs2, s.eps), 0x1p-126f);
+  return fmaf(-s.step_size, m * rcp_approx(den), __fmul_rn(p, keep));
 }
 
 template <bool Q8, int CAP>
-__global__ void __launch_bounds__(kOptThreads) adamw_kernel(const __grid_constant__ AdamwParams<CAP> a) {
+__global__ void __launch_bounds__(kOptThreads, kOptPerSm) adamw_kernel(const __grid_constant__ AdamwParams<CAP> a) {
   __shared__ StepScalars ss;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
@@ -248,135 +276,156 @@ __global__ void __launch_bounds__(kOptThreads) adamw_kernel(const __grid_constan
   __syncthreads();
   const StepScalars s = ss;
   if (!s.skip) {
-    for (int chunk = blockIdx.x; chunk < a.chunks; chunk += gridDim.x) {
-      const int k = find_tensor(a.chunk_end, a.tensors, chunk);
-      const OptTensor& t = a.t[k];
-      const long long n = t.n;
-      const long long wbase = (long long)(chunk - (k ? a.chunk_end[k - 1] : 0)) * kOptChunk + warp * kScaleBlock;
-      if (wbase >= n) continue;
-      const float keep = (float)(1.0 - s.lr * (double)t.wd);
-      float g[8], p[8], m[8], v[8], e[8];
-      const bool full = wbase + kScaleBlock <= n;
-      const float ms = Q8 ? t.ms[wbase / kScaleBlock] : 0.f, vs = Q8 ? t.vs[wbase / kScaleBlock] : 0.f;
-      if (full) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const long long i = wbase + u * 128 + lane * 4;
-          load4(t.g, t.gdt, i, g + 4 * u);
-          const float4 pv = __ldcs(reinterpret_cast<const float4*>(t.p + i));
-          p[4 * u] = pv.x; p[4 * u + 1] = pv.y; p[4 * u + 2] = pv.z; p[4 * u + 3] = pv.w;
-          if (Q8) {
-            const uint32_t mc = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(t.m) + i));
-            const uint32_t vc = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(t.v) + i));
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              m[4 * u + q] = __fmul_rn(e4m3_value((mc >> (8 * q)) & 255u), ms);
-              v[4 * u + q] = __fmul_rn(e4m3_value((vc >> (8 * q)) & 255u), vs);
-            }
-          } else {
-            const float4 mv = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(t.m) + i));
-            const float4 vv = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(t.v) + i));
-            m[4 * u] = mv.x; m[4 * u + 1] = mv.y; m[4 * u + 2] = mv.z; m[4 * u + 3] = mv.w;
-            v[4 * u] = vv.x; v[4 * u + 1] = vv.y; v[4 * u + 2] = vv.z; v[4 * u + 3] = vv.w;
-          }
-          if (t.ema) {
-            const float4 ev = __ldcs(reinterpret_cast<const float4*>(t.ema + i));
-            e[4 * u] = ev.x; e[4 * u + 1] = ev.y; e[4 * u + 2] = ev.z; e[4 * u + 3] = ev.w;
-          }
-        }
-      } else {
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {              // the tensor's end: zeros past it, which stay zero
-          const long long i = wbase + (q >> 2) * 128 + lane * 4 + (q & 3);
-          const bool in = i < n;
-          g[q] = in ? load1(t.g, t.gdt, i) : 0.f;
-          p[q] = in ? t.p[i] : 0.f;
-          if (Q8) {
-            m[q] = in ? __fmul_rn(e4m3_value(static_cast<const uint8_t*>(t.m)[i]), ms) : 0.f;
-            v[q] = in ? __fmul_rn(e4m3_value(static_cast<const uint8_t*>(t.v)[i]), vs) : 0.f;
-          } else {
-            m[q] = in ? static_cast<const float*>(t.m)[i] : 0.f;
-            v[q] = in ? static_cast<const float*>(t.v)[i] : 0.f;
-          }
-          e[q] = in && t.ema ? t.ema[i] : 0.f;
+    // From the last chunk to the first: the norm's pass has left the last gradients in L2.  What belongs to
+    // a tensor is worked out when its first chunk comes.
+    int k = a.tensors, first = a.chunks;           // the current tensor and its first chunk
+    long long n = 0;
+    float keep = 0.f;
+    uint32_t key_lo = 0, key_hi = 0;
+    for (int chunk = a.chunks - 1 - (int)blockIdx.x; chunk >= 0; chunk -= (int)gridDim.x) {
+      if (chunk < first) {
+        k = find_tensor(a.chunk_end, k, chunk);
+        first = k ? a.chunk_end[k - 1] : 0;
+        n = a.t[k].n;
+        keep = (float)(1.0 - s.lr * (double)a.t[k].wd);
+        if (Q8) {
+          const unsigned long long key = tensor_key(a.seed, s.t, a.t[k].index);
+          key_lo = (uint32_t)key;
+          key_hi = (uint32_t)(key >> 32);
         }
       }
-      float r[8];
+      const OptTensor& t = a.t[k];
+      const long long wbase = (long long)(chunk - first) * kOptChunk + warp * kScaleBlock;
+      if (wbase >= n) continue;
+      const bool full = wbase + kScaleBlock <= n, wide = t.wide;
+      const long long i0 = wbase + lane * 8;
+      const long long sb = wbase / kScaleBlock;
+      float* const tm = static_cast<float*>(t.m);
+      float* const tv = static_cast<float*>(t.v);
+      uint8_t* const qm = static_cast<uint8_t*>(t.m);
+      uint8_t* const qv = static_cast<uint8_t*>(t.v);
+      float g[8], p[8], m[8], v[8], e[8], r[8];
+      uint2 mc = make_uint2(0u, 0u), vc = mc;
+      float ms = 0.f, vs = 0.f;
+      if (Q8) {
+        ms = t.ms[sb];
+        vs = t.vs[sb];
+      }
+      if (full) {
+        ld8_grad(t.g, t.gdt, i0, wide, g);
+        ld8(t.p + i0, wide, p);
+        if (Q8) {
+          mc = *reinterpret_cast<const uint2*>(qm + i0);
+          vc = *reinterpret_cast<const uint2*>(qv + i0);
+        } else {
+          ld8(tm + i0, wide, m);
+          ld8(tv + i0, wide, v);
+        }
+        if (t.ema) ld8(t.ema + i0, wide, e);
+      } else {                                     // the tensor's end: zeros past it, which stay zero
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const bool in = i0 + q < n;
+          g[q] = in ? load1(t.g, t.gdt, i0 + q) : 0.f;
+          p[q] = in ? t.p[i0 + q] : 0.f;
+          if (Q8) {
+            if (in) {
+              (q < 4 ? mc.x : mc.y) |= (uint32_t)qm[i0 + q] << (8 * (q & 3));
+              (q < 4 ? vc.x : vc.y) |= (uint32_t)qv[i0 + q] << (8 * (q & 3));
+            }
+          } else {
+            m[q] = in ? tm[i0 + q] : 0.f;
+            v[q] = in ? tv[i0 + q] : 0.f;
+          }
+          e[q] = in && t.ema ? t.ema[i0 + q] : 0.f;
+        }
+      }
+      if (Q8) {
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const float2 a2 = e4m3_values((h < 2 ? mc.x : mc.y) >> (16 * (h & 1)) & 0xffffu);
+          const float2 b2 = e4m3_values((h < 2 ? vc.x : vc.y) >> (16 * (h & 1)) & 0xffffu);
+          m[2 * h] = __fmul_rn(a2.x, ms); m[2 * h + 1] = __fmul_rn(a2.y, ms);
+          v[2 * h] = __fmul_rn(b2.x, vs); v[2 * h + 1] = __fmul_rn(b2.y, vs);
+        }
+      }
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         if (Q8) v[q] = __fmul_rn(v[q], v[q]);      // what is stored is the root
         r[q] = moments(__fmul_rn(g[q], s.scale), m[q], v[q], s);
         p[q] = update(p[q], m[q], r[q], keep, s);
-        e[q] = t.ema ? __fadd_rn(__fmul_rn(s.ed, e[q]), __fmul_rn(s.omed, p[q])) : 0.f;
       }
-      uint32_t mc[8], vc[8];
       if (Q8) {
-        uint32_t mb = 0, vb = 0;                   // non-negative floats order as their bits do
+        float mx = 0.f, vx = 0.f;
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          mb = max(mb, __float_as_uint(fabsf(m[q])));
-          vb = max(vb, __float_as_uint(r[q]));
+          mx = max_nan(mx, fabsf(m[q]));
+          vx = max_nan(vx, r[q]);
         }
-        const float mx = __uint_as_float(__reduce_max_sync(0xffffffffu, mb));
-        const float vx = __uint_as_float(__reduce_max_sync(0xffffffffu, vb));
+        // non-negative floats order as their bits do, and a NaN lies above them
+        mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
+        vx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vx)));
         // a block whose largest moment is below 2^-100, or not finite, becomes zero
         const bool mok = mx >= 7.888609052210118e-31f && mx < INFINITY, vok = vx >= 7.888609052210118e-31f && vx < INFINITY;
-        const float mi = mok ? __fdiv_rn(448.f, mx) : 0.f, vi = vok ? __fdiv_rn(448.f, vx) : 0.f;
-        const unsigned long long key = tensor_key(a.seed, s.t, t.index);
-        const uint32_t klo = (uint32_t)key, khi = (uint32_t)(key >> 32);
+        const float mi = mok ? __fmul_rn(__frcp_rn(mx), 448.f) : 0.f, vi = vok ? __fmul_rn(__frcp_rn(vx), 448.f) : 0.f;
+        const uint32_t klo = key_lo + (uint32_t)i0;
+        if (!mok) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) m[q] = 0.f;
+        }
+        if (!vok) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) r[q] = 0.f;
+        }
+        uint32_t zm[8], zv[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          const uint32_t rnd = element_bits((uint32_t)(wbase + (q >> 2) * 128 + lane * 4 + (q & 3)), klo, khi);
-          mc[q] = e4m3_code(__fmul_rn(m[q], mi), rnd & 0xffffu);
-          vc[q] = e4m3_code(__fmul_rn(r[q], vi), rnd >> 16);
+          const uint32_t rnd = element_bits(klo + q, key_hi);
+          zm[q] = e4m3_random(__fmul_rn(m[q], mi), __byte_perm(rnd, 0u, 0x4104)) | (__float_as_uint(m[q]) & 0x80000000u);
+          zv[q] = e4m3_random(__fmul_rn(r[q], vi), __byte_perm(rnd, 0u, 0x4324));
         }
+        mc = make_uint2(top_bytes(zm[0], zm[1], zm[2], zm[3]), top_bytes(zm[4], zm[5], zm[6], zm[7]));
+        vc = make_uint2(top_bytes(zv[0], zv[1], zv[2], zv[3]), top_bytes(zv[4], zv[5], zv[6], zv[7]));
         if (lane == 0) {
-          t.ms[wbase / kScaleBlock] = mok ? __fdiv_rn(mx, 448.f) : 0.f;
-          t.vs[wbase / kScaleBlock] = vok ? __fdiv_rn(vx, 448.f) : 0.f;
+          t.ms[sb] = mok ? __fmul_rn(mx, 1.f / 448.f) : 0.f;
+          t.vs[sb] = vok ? __fmul_rn(vx, 1.f / 448.f) : 0.f;
         }
       }
       if (full) {
+        st8(t.p + i0, wide, p);
+        if (Q8) {
+          *reinterpret_cast<uint2*>(qm + i0) = mc;
+          *reinterpret_cast<uint2*>(qv + i0) = vc;
+        } else {
+          st8(tm + i0, wide, m);
+          st8(tv + i0, wide, v);
+        }
+        if (t.ema) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const long long i = wbase + u * 128 + lane * 4;
-          __stcs(reinterpret_cast<float4*>(t.p + i), make_float4(p[4 * u], p[4 * u + 1], p[4 * u + 2], p[4 * u + 3]));
-          if (Q8) {
-            uint32_t mw = 0, vw = 0;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              mw |= mc[4 * u + q] << (8 * q);
-              vw |= vc[4 * u + q] << (8 * q);
-            }
-            __stcs(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(t.m) + i), mw);
-            __stcs(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(t.v) + i), vw);
-          } else {
-            __stcs(reinterpret_cast<float4*>(static_cast<float*>(t.m) + i),
-                   make_float4(m[4 * u], m[4 * u + 1], m[4 * u + 2], m[4 * u + 3]));
-            __stcs(reinterpret_cast<float4*>(static_cast<float*>(t.v) + i),
-                   make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]));
-          }
-          if (t.ema)
-            __stcs(reinterpret_cast<float4*>(t.ema + i), make_float4(e[4 * u], e[4 * u + 1], e[4 * u + 2], e[4 * u + 3]));
-          if (t.w) {
-            const uint2 w = t.wdt == 1 ? make_uint2(pack_bf16x2(p[4 * u], p[4 * u + 1]), pack_bf16x2(p[4 * u + 2], p[4 * u + 3]))
-                                       : make_uint2(pack_f16x2(p[4 * u], p[4 * u + 1]), pack_f16x2(p[4 * u + 2], p[4 * u + 3]));
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(t.w) + i) = w;   // the next forward reads it: kept in L2
-          }
+          for (int q = 0; q < 8; ++q) e[q] = __fadd_rn(__fmul_rn(s.ed, e[q]), __fmul_rn(s.omed, p[q]));
+          st8(t.ema + i0, wide, e);
+        }
+        if (t.w) {                                 // the next forward reads it: left in L2
+          const uint4 w = t.wdt == 1 ? make_uint4(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]),
+                                                  pack_bf16x2(p[4], p[5]), pack_bf16x2(p[6], p[7]))
+                                     : make_uint4(pack_f16x2(p[0], p[1]), pack_f16x2(p[2], p[3]),
+                                                  pack_f16x2(p[4], p[5]), pack_f16x2(p[6], p[7]));
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(t.w) + i0) = w;
         }
       } else {
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          const long long i = wbase + (q >> 2) * 128 + lane * 4 + (q & 3);
+          const long long i = i0 + q;
           if (i >= n) continue;
           t.p[i] = p[q];
           if (Q8) {
-            static_cast<uint8_t*>(t.m)[i] = (uint8_t)mc[q];
-            static_cast<uint8_t*>(t.v)[i] = (uint8_t)vc[q];
+            qm[i] = (uint8_t)((q < 4 ? mc.x : mc.y) >> (8 * (q & 3)));
+            qv[i] = (uint8_t)((q < 4 ? vc.x : vc.y) >> (8 * (q & 3)));
           } else {
-            static_cast<float*>(t.m)[i] = m[q];
-            static_cast<float*>(t.v)[i] = v[q];
+            tm[i] = m[q];
+            tv[i] = v[q];
           }
-          if (t.ema) t.ema[i] = e[q];
+          if (t.ema) t.ema[i] = __fadd_rn(__fmul_rn(s.ed, e[q]), __fmul_rn(s.omed, p[q]));
           if (t.w && t.wdt == 1) static_cast<__nv_bfloat16*>(t.w)[i] = __float2bfloat16_rn(p[q]);
           else if (t.w) static_cast<__half*>(t.w)[i] = __float2half_rn(p[q]);
         }
@@ -423,6 +472,7 @@ cudaError_t norm_launch(const moe_adamw_tensor_t* t, int n, double mult, double 
     a.g[a.tensors] = t[i].grad;
     a.n[a.tensors] = t[i].n;
     a.dtype[a.tensors] = (uint8_t)t[i].grad_dtype;
+    a.wide[a.tensors] = ((uintptr_t)t[i].grad & 31u) == 0;
     a.chunk_end[a.tensors++] = (int)chunks;
   }
   a.chunks = (int)chunks;
@@ -452,6 +502,10 @@ cudaError_t adamw_launch(const moe_adamw_t& h, const moe_adamw_tensor_t* t, int 
     o.ema = t[i].ema;
     o.n = t[i].n; o.wd = t[i].weight_decay; o.index = i;
     o.gdt = (uint8_t)t[i].grad_dtype; o.wdt = (uint8_t)t[i].weight_dtype;
+    uintptr_t at = (uintptr_t)o.p | (uintptr_t)o.ema;
+    if (o.gdt == MOE_F32) at |= (uintptr_t)o.g;
+    if (!Q8) at |= (uintptr_t)o.m | (uintptr_t)o.v;
+    o.wide = (at & 31u) == 0;
     a.chunk_end[a.tensors++] = (int)chunks;
   }
   a.chunks = (int)chunks;
@@ -459,7 +513,7 @@ cudaError_t adamw_launch(const moe_adamw_t& h, const moe_adamw_tensor_t* t, int 
   a.lr = h.lr; a.beta1 = h.beta1; a.beta2 = h.beta2; a.eps = h.eps; a.ema_decay = h.ema_decay; a.mult = h.grad_mult;
   a.seed = h.seed;
   a.ctl = ctl;
-  const long long most = (long long)sms * 4;
+  const long long most = (long long)sms * kOptPerSm;   // one wave
   const int grid = (int)(chunks < 1 ? 1 : chunks < most ? chunks : most);
   adamw_kernel<Q8, CAP><<<grid, kOptThreads, 0, s>>>(a);
   return cudaGetLastError();

@@ -52,24 +52,51 @@ class _Control:
         self.skipped = self.ctl[40:48].view(torch.int64)         # steps that a non-finite gradient left out
         self._ws = None
 
+        self._ctl_ptr, self._ws_for = self.ctl.data_ptr(), -1
+
     def _init(self, step, betas):
         with torch.cuda.device(self.device):
             B.moe_optim_init(self.ctl, step, betas[0], betas[1], _stream(self.device))
 
-    def _norm(self, tensors, n, max_norm, grad_mult):
-        need = B.moe_grad_norm_workspace_size(n)
-        if self._ws is None or self._ws.numel() < need:
-            self._ws = torch.empty(need, dtype=torch.uint8, device=self.device)
-        B.moe_grad_norm(tensors, n, grad_mult, max_norm, self.ctl, self._ws, self._ws.numel(), _stream(self.device))
+    def _norm(self, tensors, n, max_norm, grad_mult, stream):
+        if self._ws_for < n:
+            self._ws = torch.empty(B.moe_grad_norm_workspace_size(n), dtype=torch.uint8, device=self.device)
+            self._ws_ptr, self._ws_bytes, self._ws_for = self._ws.data_ptr(), self._ws.numel(), n
+        B.moe_grad_norm(tensors, n, grad_mult, max_norm, self._ctl_ptr, self._ws_ptr, self._ws_bytes, stream)
+
+    def _on_device(self, call, *args):
+        """The call with the tensors' device current."""
+        if torch.cuda.current_device() == self.device.index:
+            return call(*args)
+        with torch.cuda.device(self.device):
+            return call(*args)
 
 
-def _fill_grads(tensors, grads, device, sizes=None):
-    for i, (t, g) in enumerate(zip(tensors, grads)):
-        if g is None:
-            t.n = 0                                  # no gradient: the tensor stays as it is
-            continue
-        _check(g, f"grads[{i}]", tuple(_DTYPE), device, None if sizes is None else sizes[i])
-        t.grad, t.n, t.grad_dtype = g.data_ptr(), g.numel(), _DTYPE[g.dtype]
+class _GradList:
+    """The C array of a call's tensors; a call checks its gradients and writes what differs from the last one's."""
+
+    def __init__(self, n, sizes=None):
+        self.tensors = (B.MoeAdamwTensor * n)()
+        self.sizes = sizes
+        self.items = list(self.tensors)              # ctypes makes a new view at every access
+        self.held = [None] * n
+
+    def fill(self, grads, device):
+        index, sizes, held = device.index, self.sizes, self.held
+        for i, g in enumerate(grads):
+            if g is None:
+                if held[i] is not False:
+                    self.items[i].n, held[i] = 0, False   # no gradient: the tensor stays as it is
+                continue
+            if type(g) is not torch.Tensor or g.get_device() != index or not g.is_contiguous():
+                _check(g, f"grads[{i}]", tuple(_DTYPE), device)
+            dt, n = _DTYPE.get(g.dtype), g.numel()
+            if dt is None or (sizes is not None and n != sizes[i]):
+                _check(g, f"grads[{i}]", tuple(_DTYPE), device, None if sizes is None else sizes[i])
+            new = (g.data_ptr(), n, dt)
+            if held[i] != new:
+                t = self.items[i]
+                t.grad, t.n, t.grad_dtype = held[i] = new
 
 
 class GradNorm(_Control):
@@ -81,15 +108,14 @@ class GradNorm(_Control):
     def __init__(self, device="cuda:0"):
         super().__init__(device)
         self._init(0, (0.0, 0.0))
-        self._tensors = None
+        self._list = _GradList(0)
 
     def __call__(self, grads: Sequence[Optional[torch.Tensor]], max_norm: float = 0.0, grad_mult: float = 1.0):
         n = len(grads)
-        if self._tensors is None or len(self._tensors) != n:
-            self._tensors = (B.MoeAdamwTensor * n)()
-        _fill_grads(self._tensors, grads, self.device)
-        with torch.cuda.device(self.device):
-            self._norm(self._tensors, n, max_norm, grad_mult)
+        if len(self._list.items) != n:
+            self._list = _GradList(n)
+        self._list.fill(grads, self.device)
+        self._on_device(self._norm, self._list.tensors, n, max_norm, grad_mult, _stream(self.device))
         return self.grad_norm, self.grad_scale
 
 
@@ -147,9 +173,9 @@ class AdamW(_Control):
                 self.buffers["ema"][at:at + p.numel()].copy_(p.reshape(-1))
         self.settings = B.MoeAdamw(lr, self.betas[0], self.betas[1], eps, 0.0 if ema_decay is None else ema_decay, 1.0,
                                    seed % (1 << 64), B.MOE_MOMENTS_E4M3 if q8 else B.MOE_MOMENTS_F32, 0)
-        self._tensors = (B.MoeAdamwTensor * len(params))()
+        self._list = _GradList(len(params), self.sizes)
         at = {k: b.data_ptr() for k, b in self.buffers.items()}
-        for t, p, w, wd, s in zip(self._tensors, params, weights, decay, self.starts):
+        for t, p, w, wd, s in zip(self._list.items, params, weights, decay, self.starts):
             t.param, t.weight_decay = p.data_ptr(), wd
             if w is not None:
                 t.weight, t.weight_dtype = w.data_ptr(), _DTYPE[w.dtype]
@@ -186,14 +212,16 @@ class AdamW(_Control):
         leaves everything as it is and counts in ``skipped``."""
         if len(grads) != len(self.params):
             raise ValueError(f"{len(grads)} gradients for {len(self.params)} tensors")
-        _fill_grads(self._tensors, grads, self.device, self.sizes)
-        n = len(self.params)
-        with torch.cuda.device(self.device):
-            if max_norm is not None:
-                self._norm(self._tensors, n, max_norm, grad_mult)
-            self.settings.clipped = int(max_norm is not None)
-            self.settings.grad_mult = grad_mult
-            B.moe_adamw_step(self.settings, self._tensors, n, self.ctl, _stream(self.device))
+        self._list.fill(grads, self.device)
+        self._on_device(self._step_now, max_norm, grad_mult, _stream(self.device))
+
+    def _step_now(self, max_norm, grad_mult, stream):
+        tensors, n, settings = self._list.tensors, len(self.params), self.settings
+        if max_norm is not None:
+            self._norm(tensors, n, max_norm, grad_mult, stream)
+        settings.clipped = int(max_norm is not None)
+        settings.grad_mult = grad_mult
+        B.moe_adamw_step(settings, tensors, n, self._ctl_ptr, stream)
 
     def state_dict(self) -> dict:
         """Copies of the state and the step count (waits for the device)."""
