@@ -1137,7 +1137,8 @@ static SbLayout sb_layout(const moe_config_t* c) {
   L.frag = take(is16(c) ? nblk * seq_balance_frag_bytes(c->E, c->dtype) : 0);
   L.scales = take(c->dtype == MOE_F16 ? nblk * 128 : 0);
   L.dl = take(is16(c) ? 0 : T * ep * 4);
-  L.db_part = take(is16(c) ? nblk * ep * 4 : 0);
+  // rows of the two kernels' token blocks, or four router warps of each block of the fused one
+  L.db_part = take(is16(c) ? (nblk > 4 * (size_t)groups ? nblk : 4 * (size_t)groups) * ep * 4 : 0);
   L.partials = take((size_t)groups * c->E * c->D * 4);
   L.total = off;
   return L;
@@ -1199,7 +1200,7 @@ int moe_seq_balance(const moe_config_t* cfg, const void* x, const void* wg, cons
   SeqBalArgs a{};
   a.x = x; a.wg = wg; a.bias = router_bias;
   a.T = cfg->T; a.D = cfg->D; a.E = cfg->E; a.K = cfg->K; a.Kmax = kmax_of(cfg); a.dtype = cfg->dtype;
-  a.alpha = cfg->alpha; a.aux_scale = aux_scale;
+  a.factor = (float)((double)cfg->alpha * cfg->E / cfg->K); a.aux_scale = aux_scale;
   a.offsets = seq_offsets; a.n_seqs = n_seqs; a.seq_len = seq_len;
   a.topk_idx = topk_idx; a.n_sel = n_sel; a.dgate = dgate;
   a.counts = seq_counts; a.seq_loss = seq_loss; a.loss = loss;
@@ -1215,6 +1216,13 @@ int moe_seq_balance(const moe_config_t* cfg, const void* x, const void* wg, cons
   a.db_part = ws_at<float>(bws, L.db_part);
   a.partials = ws_at<float>(bws, L.partials);
   a.status = status_ptr(ws);
+  CUtensorMap tmx;
+  if (a.grads && seq_balance_fused(cfg->D, cfg->E, cfg->dtype)) {
+    if (!make_tmap_rows3d(&tmx, x, cfg->dtype, cfg->T, cfg->D, 16, cfg->D / 64))
+      return fail(MOE_ERR_CUDA, "tensor map for x failed");
+    a.tmap_x = &tmx;
+    a.fused = 1;
+  }
   if ((e = launch_seq_balance(a, s)) != cudaSuccess) return cuda_fail(e, "balance loss over sequences");
   return ok();
 }

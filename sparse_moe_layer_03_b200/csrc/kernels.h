@@ -281,7 +281,7 @@ cudaError_t launch_combine(const CombineArgs& a, cudaStream_t s);
 struct SeqBalArgs {
   const void* x; const void* wg; const float* bias;   // x [T,D], wg [E,D] act; bias [E] or null
   int T, D, E, K, Kmax, dtype;
-  float alpha, aux_scale;
+  float factor, aux_scale;                            // alpha E / K
   const int32_t* offsets; int n_seqs, seq_len;        // [n_seqs + 1] row borders, or null: seq_len rows each
   const int32_t* topk_idx; const int32_t* n_sel;      // n_sel null: K slots each
   const float* dgate;                                 // [T,Kmax] or null
@@ -289,6 +289,8 @@ struct SeqBalArgs {
   int grads;                                          // the gradients below are wanted
   float* dwg; float* dbias; void* dx; int accumulate; // dbias and dx may be null
   int groups, blocks_per_range;                       // seq_balance_plan
+  int fused;                                          // scores and grads in one kernel, which reads x by this map
+  const CUtensorMap* tmap_x;                          //   (boxes of 16 whole rows)
   // scratch
   int2* tok;                                          // [T] sequence (-1: none) and factor of its counts
   int* live;                                          // [1] sequences with a row
@@ -305,6 +307,7 @@ constexpr int kSbSms = 148;                           // the plan (and so the su
 constexpr int kSbF32Single = 148 * 32;                // fp32: tokens up to which a warp takes one at a time
 int seq_balance_ep(int E);                            // experts rounded up to 8, 16 or 32
 size_t seq_balance_frag_bytes(int E, int dtype);
+bool seq_balance_fused(int D, int E, int dtype);      // else the shape takes the two kernels
 void seq_balance_plan(int T, int D, int E, int dtype, int* groups, int* blocks_per_range);
 cudaError_t launch_seq_balance(const SeqBalArgs& a, cudaStream_t s);
 

@@ -37,7 +37,8 @@ namespace {
 
 constexpr int kCountThreads = 256;
 constexpr int kOffSmem = 2048;                     // offsets kept in shared memory up to this many
-constexpr int kCountSmall = 4096;                  // tokens, and counts, that one block takes alone
+constexpr int kOneThreads = 1024;
+constexpr int kOneTokens = 2048, kOneCounts = 4096;   // most tokens and counts of the one-block form
 constexpr int kFinThreads = 256;
 
 // 16 bytes into this lane's own slot (zeros where !in): read back by the lane alone, after cp_wait
@@ -64,25 +65,42 @@ __device__ __forceinline__ int slots_of(const SeqBalArgs& a, int t) {
 }
 
 // ---------------------------------------------------------------- count
-// One thread per token: its sequence by binary search, its selected experts into the counts (equal
-// (sequence, expert) keys of a warp merged first, as in the frequency kernel).  SMALL: one block, the
-// counts in shared memory.  T = 512: 1.9 us less than clearing and adding to them in global memory.
-template <bool SMALL>
-__global__ void __launch_bounds__(SMALL ? 1024 : kCountThreads) seq_count_kernel(SeqBalArgs a) {
+// One thread per token: its sequence by binary search, its selected experts into the counts.  ONE: one
+// block, the counts in shared memory; no clearing, no global atomics.  Else equal (sequence, expert) keys of
+// a warp are merged (as in the frequency kernel) and added to counts that were cleared before.  The choice
+// is by the tokens: a cluster of eight blocks adding up their shared memory took 9.3 us for 32768 tokens
+// (half of it more blocks' work: 128 blocks and clearing 6.5), and gained nothing from 10000 down.
+template <bool ONE>
+__global__ void __launch_bounds__(ONE ? kOneThreads : kCountThreads) seq_count_kernel(SeqBalArgs a) {
   __shared__ int off_s[kOffSmem];
-  __shared__ int hist[SMALL ? kCountSmall : 1];
+  __shared__ int hist[ONE ? kOneCounts : 1];
   __shared__ int full_s;
   launch_dependents();
   const int tid = threadIdx.x, n = a.n_seqs, nt = blockDim.x;
+  constexpr int kAhead = 4;                        // slots loaded with the token
   const int* off = a.offsets;
   const bool in_smem = n + 1 <= kOffSmem;
-  if (SMALL)
+  if (ONE)
     for (int i = tid; i < n * a.E; i += nt) hist[i] = 0;
   if (tid == 0) full_s = 0;
   if (off && in_smem) {
     for (int i = tid; i <= n; i += nt) off_s[i] = off[i];
     off = off_s;
   }
+  // a round: kRound tokens of the thread, their slots on the way together (the first round's beside the offsets)
+  constexpr int kRound = ONE ? 2 : 1;
+  const int stride = gridDim.x * nt;
+  int ns[kRound], idx[kRound][kAhead];
+  auto load_slots = [&](int t0) {
+#pragma unroll
+    for (int i = 0; i < kRound; ++i) {
+      const int t = t0 + i * stride;
+      ns[i] = t < a.T ? slots_of(a, t) : 0;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) idx[i][k] = t < a.T && k < a.Kmax ? a.topk_idx[(size_t)t * a.Kmax + k] : -1;
+    }
+  };
+  load_slots(blockIdx.x * nt + tid);
   __syncthreads();
   // sequences that hold a row: by the first block where it has the offsets at hand, else by all blocks
   if (off && (!in_smem || blockIdx.x == 0)) {
@@ -95,47 +113,57 @@ __global__ void __launch_bounds__(SMALL ? 1024 : kCountThreads) seq_count_kernel
     full = __reduce_add_sync(0xffffffffu, full);
     if ((tid & 31) == 0 && full) atomicAdd(in_smem ? &full_s : a.live, full);
   }
-  for (int t0 = blockIdx.x * nt; t0 < a.T; t0 += gridDim.x * nt) {
-    const int t = t0 + tid;
-    int sid = -1, len = 0;
-    if (t < a.T) {
-      if (off) {
-        int lo = 0, hi = n;                        // the last sequence that starts at or before t
-        while (lo < hi) {
-          const int mid = (lo + hi) >> 1;
-          if (off[mid] <= t) lo = mid + 1;
-          else hi = mid;
+  for (int first = blockIdx.x * nt; first < a.T; first += kRound * stride) {
+#pragma unroll
+    for (int i = 0; i < kRound; ++i) {
+      const int t = first + i * stride + tid;
+      int sid = -1, len = 0;
+      if (t < a.T) {
+        if (off) {
+          int lo = 0, hi = n;                      // the last sequence that starts at or before t
+          while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (off[mid] <= t) lo = mid + 1;
+            else hi = mid;
+          }
+          sid = lo - 1;
+          if (sid >= 0) {
+            len = off[sid + 1] - off[sid];
+            if (t < off[sid] || t >= off[sid + 1]) sid = -1;   // (the first holds where offsets descend)
+          }
+        } else {
+          sid = t / a.seq_len;
+          len = a.seq_len;
         }
-        sid = lo - 1;
-        if (sid >= 0) {
-          len = off[sid + 1] - off[sid];
-          if (t < off[sid] || t >= off[sid + 1]) sid = -1;   // (the first holds where offsets descend)
+        const float coef = sid >= 0 ? a.factor / ((float)len * (float)len) : 0.f;
+        a.tok[t] = make_int2(sid, __float_as_int(coef));
+      }
+      const int use = sid >= 0 ? ns[i] : 0;
+      auto add = [&](int k, int e) {               // every lane, for __match_any_sync
+        long long key = -1;
+        if (k < use) {
+          if (e >= a.E) set_status(a.status, DEV_BAD_INDEX, 411);
+          else if (e >= 0) key = (long long)sid * a.E + e;
         }
-      } else {
-        sid = t / a.seq_len;
-        len = a.seq_len;
-      }
-      const float coef = sid >= 0 ? (float)((double)a.alpha * a.E / ((double)a.K * len * len)) : 0.f;
-      a.tok[t] = make_int2(sid, __float_as_int(coef));
-    }
-    const int ns = sid >= 0 ? slots_of(a, t) : 0;
-    for (int k = 0; k < a.Kmax; ++k) {
-      long long key = -1;
-      if (k < ns) {
-        const int e = a.topk_idx[(size_t)t * a.Kmax + k];
-        if (e >= a.E) set_status(a.status, DEV_BAD_INDEX, 411);
-        else if (e >= 0) key = (long long)sid * a.E + e;
-      }
-      if (SMALL) {
-        if (key >= 0) atomicAdd(&hist[key], 1);
-      } else {
-        const unsigned same = __match_any_sync(0xffffffffu, key);
-        if (key >= 0 && (tid & 31) == __ffs(same) - 1) atomicAdd(&a.counts[key], __popc(same));
+        if (ONE) {
+          if (key >= 0) atomicAdd(&hist[key], 1);
+        } else {
+          const unsigned same = __match_any_sync(0xffffffffu, key);
+          if (key >= 0 && (tid & 31) == __ffs(same) - 1) atomicAdd(&a.counts[key], __popc(same));
+        }
+      };
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (k < a.Kmax) add(k, idx[i][k]);
+      for (int k = kAhead; k < a.Kmax; ++k) {
+        if (!__any_sync(0xffffffffu, k < use)) break;
+        add(k, k < use ? a.topk_idx[(size_t)t * a.Kmax + k] : -1);
       }
     }
+    if (first + kRound * stride < a.T) load_slots(first + kRound * stride + tid);
   }
   __syncthreads();
-  if (SMALL)
+  if (ONE)
     for (int i = tid; i < n * a.E; i += nt) a.counts[i] = hist[i];
   if (blockIdx.x == 0 && tid == 0 && (in_smem || !a.offsets)) *a.live = a.offsets ? full_s : n;
 }
@@ -178,12 +206,181 @@ template <int NE, bool F16> struct Parts {
   static constexpr int T = F16 ? A : NE == 1 ? 2 : 3 * NK;  // for dWg
 };
 
+// The gates' gradients of a 16-token block, lane l < 16 holding token l's first slots: loaded ahead of
+// their use.
+struct GatesAhead {
+  int ns, e[kGateAhead];
+  float v[kGateAhead];
+};
+__device__ __forceinline__ GatesAhead load_gates(const SeqBalArgs& a, int rb) {
+  GatesAhead q;
+  const int lane = threadIdx.x & 31, t = rb * 16 + lane;
+  const bool in = a.dgate && lane < 16 && t < a.T;
+  q.ns = in ? slots_of(a, t) : 0;
+#pragma unroll
+  for (int k = 0; k < kGateAhead; ++k) {
+    q.e[k] = in && k < a.Kmax ? a.topk_idx[(size_t)t * a.Kmax + k] : -1;
+    q.v[k] = in && k < a.Kmax ? a.dgate[(size_t)t * a.Kmax + k] : 0.f;
+  }
+  return q;
+}
+// ... scattered to their experts, each token by one lane: dp [16][ep] in shared memory
+template <int EP>
+__device__ __forceinline__ void scatter_gates(const SeqBalArgs& a, const GatesAhead& q, int rb, int t_lo, int t_hi, float* dp) {
+  const int lane = threadIdx.x & 31, t = rb * 16 + lane;
+  __syncwarp();
+  for (int i = lane; i < 16 * EP; i += 32) dp[i] = 0.f;
+  __syncwarp();
+  if (t >= t_lo && t < t_hi) {                     // ns = 0 on the other lanes
+#pragma unroll
+    for (int k = 0; k < kGateAhead; ++k)
+      if (k < q.ns && q.e[k] >= 0 && q.e[k] < a.E) dp[lane * EP + q.e[k]] += q.v[k];
+    for (int k = kGateAhead; k < q.ns; ++k) {
+      const int e = a.topk_idx[(size_t)t * a.Kmax + k];
+      if (e >= 0 && e < a.E) dp[lane * EP + e] += a.dgate[(size_t)t * a.Kmax + k];
+    }
+  }
+  __syncwarp();
+}
+
+// What a lane holds of a block: rows t0 = 16 rb + g and t0 + 8 (r = 0, 1), experts nt * 8 + 2c + q.
+template <int NE> using RowPair = float[2][NE][2];
+
+// C = factor * counts of the rows' sequences
+template <int NE>
+__device__ __forceinline__ void load_counts(const SeqBalArgs& a, const bool* live, int t0, RowPair<NE>& C, bool* in) {
+  const int c = threadIdx.x & 3;
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int2 tk = live[r] ? a.tok[t0 + 8 * r] : make_int2(-1, 0);
+    in[r] = tk.x >= 0;
+#pragma unroll
+    for (int nt = 0; nt < NE; ++nt)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int e = nt * 8 + 2 * c + q;
+        C[r][nt][q] = in[r] && e < a.E ? __int_as_float(tk.y) * (float)a.counts[(size_t)tk.x * a.E + e] : 0.f;
+      }
+  }
+}
+
+// Logits (without the bias) to dl in place; the tokens' and the block's shares of the loss are written.
+template <int NE>
+__device__ __forceinline__ void logits_to_dl(const SeqBalArgs& a, int rb, const float* dp_s, float aux, const RowPair<NE>& C,
+                                             const bool* in, RowPair<NE>& l) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, E = a.E;
+  float loss16 = 0.f;
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int nt = 0; nt < NE; ++nt)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int e = nt * 8 + 2 * c + q;
+        l[r][nt][q] = e < E ? l[r][nt][q] + (a.bias ? __ldg(a.bias + e) : 0.f) : -INFINITY;
+        m = fmaxf(m, l[r][nt][q]);
+      }
+    m = quad_max(m);
+    float z = 0.f;
+#pragma unroll
+    for (int nt = 0; nt < NE; ++nt)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        l[r][nt][q] = nt * 8 + 2 * c + q < E ? expf(l[r][nt][q] - m) : 0.f;
+        z += l[r][nt][q];
+      }
+    const float iz = 1.0f / quad_sum(z);
+    float dp[NE][2], share = 0.f, pc = 0.f;
+#pragma unroll
+    for (int nt = 0; nt < NE; ++nt)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        l[r][nt][q] *= iz;
+        share += l[r][nt][q] * C[r][nt][q];
+        dp[nt][q] = aux * C[r][nt][q] + (a.dgate ? dp_s[(g + 8 * r) * NE * 8 + nt * 8 + 2 * c + q] : 0.f);
+        pc += l[r][nt][q] * dp[nt][q];
+      }
+    share = quad_sum(share);
+    pc = quad_sum(pc);
+    share = in[r] ? share : 0.f;
+    const int t = rb * 16 + g + 8 * r;
+    if (c == 0 && t < a.T) a.tok_loss[t] = share;
+    loss16 += share;
+#pragma unroll
+    for (int nt = 0; nt < NE; ++nt)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) l[r][nt][q] = in[r] ? l[r][nt][q] * (dp[nt][q] - pc) : 0.f;
+  }
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) loss16 += __shfl_xor_sync(0xffffffffu, loss16, o);
+  if (lane == 0 && rb * 16 < a.T) a.blk_loss[rb] = loss16;
+}
+
+// dl in fragment order: fa (k = experts) for dx, ft (k = tokens, by movmatrix) for dWg, and fp16's inverse
+// scales of rows g, g + 8 and the block.
+template <int NE, bool F16>
+__device__ __forceinline__ void dl_fragments(const RowPair<NE>& dl, uint4* fa, uint4* fw, float4& scale) {
+  using H = H16<F16>;
+  using P = Parts<NE, F16>;
+  float sr[2] = {1.f, 1.f}, sb = 1.f;
+  if (F16) {
+    float mr[2], inv[2], invb;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      mr[r] = 0.f;
+#pragma unroll
+      for (int nt = 0; nt < NE; ++nt) mr[r] = fmaxf(mr[r], fmaxf(fabsf(dl[r][nt][0]), fabsf(dl[r][nt][1])));
+      mr[r] = quad_max(mr[r]);
+      sr[r] = pow2_scale(mr[r], inv[r]);
+    }
+    float mb = fmaxf(mr[0], mr[1]);
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
+    sb = pow2_scale(mb, invb);
+    scale = make_float4(inv[0], inv[1], invb, 0.f);
+  }
+  constexpr int NP = F16 ? 2 : 3;                  // parts
+  uint32_t f[2][NP][NE], ft[2][NP][NE];
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int nt = 0; nt < NE; ++nt) {
+      auto split = [](float u, float v, uint32_t* part, int stride) {   // each part what the ones before leave
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          part[i * stride] = H::pack(u, v);
+          const float2 h = H::unpack(part[i * stride]);
+          u -= h.x;
+          v -= h.y;
+        }
+      };
+      split(dl[r][nt][0] * sr[r], dl[r][nt][1] * sr[r], &f[r][0][nt], NE);
+      if (F16) split(dl[r][nt][0] * sb, dl[r][nt][1] * sb, &ft[r][0][nt], NE);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) ft[r][i][nt] = movm_t(F16 ? ft[r][i][nt] : f[r][i][nt]);
+    }
+  if (NE == 1) {                                   // k (or m) = 0..7 the first part, 8..15 the second; then the third
+    fa[0] = make_uint4(f[0][0][0], f[1][0][0], f[0][1][0], f[1][1][0]);
+    fw[0] = make_uint4(ft[0][0][0], ft[0][1][0], ft[1][0][0], ft[1][1][0]);
+    if (NP == 3) fw[P::T - 1] = make_uint4(ft[0][NP - 1][0], 0u, ft[1][NP - 1][0], 0u);
+  } else {
+#pragma unroll
+    for (int p = 0; p < P::NK; ++p)
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {               // 16 experts: part after part
+        constexpr int o = NE > 1;
+        if (i < 2) fa[2 * p + i] = make_uint4(f[0][i][2 * p], f[1][i][2 * p], f[0][i][2 * p + o], f[1][i][2 * p + o]);
+        fw[NP * p + i] = make_uint4(ft[0][i][2 * p], ft[0][i][2 * p + o], ft[1][i][2 * p], ft[1][i][2 * p + o]);
+      }
+  }
+}
+
 // One warp per 16 tokens.  NE: 8-expert tiles of the logits.  In a k32 step lane (g, c) (g = lane / 4,
 // c = lane % 4) holds columns 8c .. 8c+7 of rows g and g + 8 of x and of row g of each 8 rows of Wg:
 // the first four of them serve as k = 2c, 2c+1, 2c+8, 2c+9 of one k16 product, the others of a second.
 template <int NE, bool F16>
 __global__ void __launch_bounds__(kScWarps * 32) seq_scores_kernel(SeqBalArgs a) {
-  using H = H16<F16>;
   constexpr int EP = NE * 8;
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float dp_s[kScWarps][16][EP];
@@ -208,20 +405,10 @@ __global__ void __launch_bounds__(kScWarps * 32) seq_scores_kernel(SeqBalArgs a)
     }
     cp_commit();
   }
-  // what the rest needs of the token of this lane (lanes 0..15), on its way meanwhile
-  const int tl = rb * 16 + lane;
-  const bool gated = a.dgate && lane < 16 && tl < a.T;
-  const int ns = gated ? slots_of(a, tl) : 0;
-  int ge[kGateAhead];
-  float gv[kGateAhead];
-#pragma unroll
-  for (int k = 0; k < kGateAhead; ++k) {
-    ge[k] = gated && k < a.Kmax ? a.topk_idx[(size_t)tl * a.Kmax + k] : -1;
-    gv[k] = gated && k < a.Kmax ? a.dgate[(size_t)tl * a.Kmax + k] : 0.f;
-  }
+  const GatesAhead gates = load_gates(a, rb);      // on their way meanwhile
   int t_lo, t_hi;
   live_rows(a, t_lo, t_hi);
-  const bool v0 = t0 >= t_lo && t0 < t_hi, v1 = t1 >= t_lo && t1 < t_hi;
+  const bool live[2] = {t0 >= t_lo && t0 < t_hi, t1 >= t_lo && t1 < t_hi};
   float acc[NE][2][4];
 #pragma unroll
   for (int nt = 0; nt < NE; ++nt)
@@ -250,153 +437,39 @@ __global__ void __launch_bounds__(kScWarps * 32) seq_scores_kernel(SeqBalArgs a)
     cp_commit();
     slot = slot + 1 == kScRing ? 0 : slot + 1;
   }
-  // lane (g, c): logits of rows t0 and t1 (r = 0, 1), experts nt * 8 + 2c and + 1
-  float l[2][NE][2];
+  RowPair<NE> l, C;
 #pragma unroll
   for (int nt = 0; nt < NE; ++nt)
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int e = nt * 8 + 2 * c + q;
-      const float b = e < E && a.bias ? a.bias[e] : 0.f;
+    for (int q = 0; q < 2; ++q)
 #pragma unroll
-      for (int r = 0; r < 2; ++r) l[r][nt][q] = e < E ? acc[nt][0][2 * r + q] + acc[nt][1][2 * r + q] + b : -INFINITY;
-    }
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {                    // softmax
-    float m = -INFINITY;
-#pragma unroll
-    for (int nt = 0; nt < NE; ++nt) m = fmaxf(m, fmaxf(l[r][nt][0], l[r][nt][1]));
-    m = quad_max(m);
-    float z = 0.f;
-#pragma unroll
-    for (int nt = 0; nt < NE; ++nt)
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        l[r][nt][q] = nt * 8 + 2 * c + q < E ? expf(l[r][nt][q] - m) : 0.f;
-        z += l[r][nt][q];
-      }
-    const float iz = 1.0f / quad_sum(z);
-#pragma unroll
-    for (int nt = 0; nt < NE; ++nt)
-#pragma unroll
-      for (int q = 0; q < 2; ++q) l[r][nt][q] *= iz;
-  }
-  // the gates' gradients of the 16 tokens: scattered to their experts, each token by one lane
-  if (a.dgate) {
-    float* dp = &dp_s[w][0][0];
-    for (int i = lane; i < 16 * EP; i += 32) dp[i] = 0.f;
-    __syncwarp();
-    if (tl >= t_lo && tl < t_hi) {                 // ns = 0 on the other lanes
-#pragma unroll
-      for (int k = 0; k < kGateAhead; ++k)
-        if (k < ns && ge[k] >= 0 && ge[k] < E) dp[lane * EP + ge[k]] += gv[k];
-      for (int k = kGateAhead; k < ns; ++k) {
-        const int e = a.topk_idx[(size_t)tl * a.Kmax + k];
-        if (e >= 0 && e < E) dp[lane * EP + e] += a.dgate[(size_t)tl * a.Kmax + k];
-      }
-    }
-    __syncwarp();
-  }
+      for (int r = 0; r < 2; ++r) l[r][nt][q] = acc[nt][0][2 * r + q] + acc[nt][1][2 * r + q];
+  if (a.dgate) scatter_gates<EP>(a, gates, rb, t_lo, t_hi, &dp_s[w][0][0]);
   grid_dependency_wait();                          // from here on: what count wrote
-  const float aux = a.aux_scale / (float)max(*a.live, 1);
-  float dl[2][NE][2], loss16 = 0.f;
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int t = r ? t1 : t0;
-    const bool live = r ? v1 : v0;
-    const int2 tk = live ? a.tok[t] : make_int2(-1, 0);
-    const float coef = __int_as_float(tk.y);
-    float dp[NE][2], share = 0.f, pc = 0.f;
-#pragma unroll
-    for (int nt = 0; nt < NE; ++nt)
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int e = nt * 8 + 2 * c + q;
-        const float C = tk.x >= 0 && e < E ? coef * (float)a.counts[(size_t)tk.x * E + e] : 0.f;
-        share += l[r][nt][q] * C;
-        dp[nt][q] = aux * C + (a.dgate ? dp_s[w][g + 8 * r][e] : 0.f);
-        pc += l[r][nt][q] * dp[nt][q];
-      }
-    share = quad_sum(share);
-    pc = quad_sum(pc);
-    share = tk.x >= 0 ? share : 0.f;
-    if (c == 0 && t < a.T) a.tok_loss[t] = share;
-    loss16 += share;
-#pragma unroll
-    for (int nt = 0; nt < NE; ++nt)
-#pragma unroll
-      for (int q = 0; q < 2; ++q) dl[r][nt][q] = tk.x >= 0 ? l[r][nt][q] * (dp[nt][q] - pc) : 0.f;
-  }
-  if (rb * 16 >= a.T) return;
-#pragma unroll
-  for (int o = 4; o < 32; o <<= 1) loss16 += __shfl_xor_sync(0xffffffffu, loss16, o);
-  if (lane == 0) a.blk_loss[rb] = loss16;
-  if (!a.grads) return;
+  bool in[2];
+  load_counts<NE>(a, live, t0, C, in);
+  logits_to_dl<NE>(a, rb, &dp_s[w][0][0], a.aux_scale / (float)max(*a.live, 1), C, in, l);
+  if (!a.grads || rb * 16 >= a.T) return;
   // db of the 16 tokens
 #pragma unroll
   for (int nt = 0; nt < NE; ++nt)
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      float s = dl[0][nt][q] + dl[1][nt][q];
+      float sum = l[0][nt][q] + l[1][nt][q];
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (g == 0) a.db_part[(size_t)rb * EP + nt * 8 + 2 * c + q] = s;
+      for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (g == 0) a.db_part[(size_t)rb * EP + nt * 8 + 2 * c + q] = sum;
     }
-  // fragments of dl and of its transpose
-  float sr[2] = {1.f, 1.f}, sb = 1.f;
-  if (F16) {
-    float mr[2], inv[2], invb;
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      mr[r] = 0.f;
-#pragma unroll
-      for (int nt = 0; nt < NE; ++nt) mr[r] = fmaxf(mr[r], fmaxf(fabsf(dl[r][nt][0]), fabsf(dl[r][nt][1])));
-      mr[r] = quad_max(mr[r]);
-      sr[r] = pow2_scale(mr[r], inv[r]);
-    }
-    float mb = fmaxf(mr[0], mr[1]);
-#pragma unroll
-    for (int o = 4; o < 32; o <<= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
-    sb = pow2_scale(mb, invb);
-    if (c == 0) a.scales[(size_t)rb * 8 + g] = make_float4(inv[0], inv[1], invb, 0.f);
-  }
   using P = Parts<NE, F16>;
-  constexpr int NP = F16 ? 2 : 3;                  // parts
-  uint32_t f[2][NP][NE], ft[2][NP][NE];
+  uint4 fa[P::A], fw[P::T];
+  float4 scale;
+  dl_fragments<NE, F16>(l, fa, fw, scale);
+  if (F16 && c == 0) a.scales[(size_t)rb * 8 + g] = scale;
+  uint4* out = a.frag + (size_t)rb * (P::A + P::T) * 32 + lane;
 #pragma unroll
-  for (int r = 0; r < 2; ++r)
+  for (int i = 0; i < P::A; ++i) out[i * 32] = fa[i];
 #pragma unroll
-    for (int nt = 0; nt < NE; ++nt) {
-      auto split = [](float u, float v, uint32_t* part, int stride) {   // each part what the ones before leave
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          part[i * stride] = H::pack(u, v);
-          const float2 h = H::unpack(part[i * stride]);
-          u -= h.x;
-          v -= h.y;
-        }
-      };
-      split(dl[r][nt][0] * sr[r], dl[r][nt][1] * sr[r], &f[r][0][nt], NE);
-      if (F16) split(dl[r][nt][0] * sb, dl[r][nt][1] * sb, &ft[r][0][nt], NE);
-#pragma unroll
-      for (int i = 0; i < NP; ++i) ft[r][i][nt] = movm_t(F16 ? ft[r][i][nt] : f[r][i][nt]);
-    }
-  uint4* fa = a.frag + (size_t)rb * (P::A + P::T) * 32 + lane;
-  uint4* fw = fa + P::A * 32;
-  if (NE == 1) {                                   // k (or m) = 0..7 the first part, 8..15 the second; then the third
-    fa[0] = make_uint4(f[0][0][0], f[1][0][0], f[0][1][0], f[1][1][0]);
-    fw[0] = make_uint4(ft[0][0][0], ft[0][1][0], ft[1][0][0], ft[1][1][0]);
-    if (NP == 3) fw[32] = make_uint4(ft[0][NP - 1][0], 0u, ft[1][NP - 1][0], 0u);
-  } else {
-#pragma unroll
-    for (int p = 0; p < P::NK; ++p)
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {               // 16 experts: part after part
-        constexpr int o = NE > 1;
-        if (i < 2) fa[(2 * p + i) * 32] = make_uint4(f[0][i][2 * p], f[1][i][2 * p], f[0][i][2 * p + o], f[1][i][2 * p + o]);
-        fw[(NP * p + i) * 32] = make_uint4(ft[0][i][2 * p], ft[0][i][2 * p + o], ft[1][i][2 * p], ft[1][i][2 * p + o]);
-      }
-  }
+  for (int i = 0; i < P::T; ++i) out[(P::A + i) * 32] = fw[i];
 }
 
 // ---------------------------------------------------------------- grads, 16-bit types
@@ -595,6 +668,389 @@ __global__ void __launch_bounds__(128, NE == 4 ? 2 : 3) seq_grads_kernel(SeqBalA
   }
 }
 
+// ---------------------------------------------------------------- scores and grads in one, 16-bit types
+// One block of 16 warps an SM over every grid-th 16-token block; x comes in once, by TMA, into a ring of
+// whole blocks of rows (64-column boxes, 128-byte swizzle) and leaves it when both halves are done:
+//   4 router warps, a token block each in turn: logits (ldmatrix and mma.sync on the stage), softmax, dl,
+//     left in shared memory in fragment order;
+//   12 column warps, each a slice of 32-column groups over all the block's tokens: dWg in registers from
+//     the stage (transposed ldmatrix), dx from dl and the gate weight's columns in registers.
+// They meet on mbarriers only (dl full and empty by router, x full by stage); the last column warp to leave
+// a stage refills it.  For E <= 16 and rows of at most 1152.
+constexpr int kFuRouters = 4, kFuCols = 12, kFuThreads = (kFuRouters + kFuCols) * 32;
+constexpr int kFuGroups = 3;                       // 32-column groups a column warp holds
+constexpr int kFuMaxStages = 6;
+constexpr int kFuMaxSmem = 232448;
+
+struct FusedSmem { int wg_stride, x, wg, dl, dl_slot, dp, old, misc, total, stage; };
+// most 32-column groups a column warp holds
+__host__ __device__ inline int fused_groups(int D) { return (D / 32 + kFuCols - 1) / kFuCols; }
+// `held`: blocks whose slices of dx, to be added to, are on their way (0: dx is not added to)
+__host__ __device__ inline FusedSmem fused_smem(int D, int ne, int frags, int stages, int held) {
+  FusedSmem L;
+  L.stage = 16 * D * 2;
+  L.wg_stride = D * 2 + 16;
+  L.dl_slot = frags * 512 + 128;
+  L.x = 0;
+  L.wg = stages * L.stage;
+  L.dl = L.wg + ne * 8 * L.wg_stride;
+  L.dp = L.dl + kFuRouters * L.dl_slot;
+  L.old = L.dp + kFuRouters * 16 * ne * 8 * 4;
+  L.misc = L.old + held * kFuCols * fused_groups(D) * 1024;
+  L.total = L.misc + 256 + 1024;                   // barriers and counters; alignment of the stages
+  return L;
+}
+// Stages of x and blocks of dx in flight.  Two blocks of dx where three stages fit beside them, else one:
+// XL with 8 experts 57.5 us with (3, 2) against 62.5 with (4, 1); with 16, 88.3 with (2, 2) against 72.7
+// with (3, 1).
+struct FusedPlan { int stages, held; };
+__host__ inline FusedPlan fused_plan(int D, int ne, int frags, bool add) {
+  for (int held = add ? 2 : 0;; --held) {
+    int n = kFuMaxStages;
+    while (n > 0 && fused_smem(D, ne, frags, n, held).total > kFuMaxSmem) --n;
+    if (n >= 3 || held <= 1) return {n, held};
+  }
+}
+
+// Bounded wait until `need` loads have been issued into a stage.  A router may be a whole turn of the ring
+// ahead, and a parity cannot tell its phase from the one two before: once the load is issued the phases
+// before it are over, and the parity is unambiguous.
+__device__ __forceinline__ bool wait_issued(volatile int* loads, int need, volatile int* abort_flag, int* status, int where) {
+  if (*loads >= need) return true;
+  const uint64_t t0 = global_ns();
+#pragma unroll 1
+  while (*loads < need) {
+    if (*abort_flag) return false;
+    __nanosleep(64);                               // the column warps need the issue slots
+    if (global_ns() - t0 > kWaitLimitNs) {
+      set_status(status, DEV_TIMEOUT, where);
+      *abort_flag = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
+template <int NE, bool F16>
+__global__ void __launch_bounds__(kFuThreads, 1)
+seq_fused_kernel(const __grid_constant__ CUtensorMap tmap_x, const SeqBalArgs a, const int stages, const int held_blocks) {
+  using H = H16<F16>;
+  using P = Parts<NE, F16>;
+  constexpr int EP = NE * 8;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  const bool add = held_blocks > 0;
+  const FusedSmem L = fused_smem(a.D, NE, P::A + P::T, stages, held_blocks);
+  const int D = a.D, E = a.E, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int g = lane >> 2, c = lane & 3, li = lane >> 3, lj = lane & 7;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L.misc);
+  uint64_t* dl_full = full + kFuMaxStages;
+  uint64_t* dl_empty = dl_full + kFuRouters;
+  uint64_t* wbar = dl_empty + kFuRouters;
+  int* done = reinterpret_cast<int*>(wbar + 1);    // column warps that left a stage
+  volatile int* loads = done + kFuMaxStages;       // loads issued into a stage
+  volatile int* abort_flag = loads + kFuMaxStages;
+  launch_dependents();
+  int t_lo, t_hi;
+  live_rows(a, t_lo, t_hi);
+  const int b_lo = t_lo / 16, b_hi = t_hi > t_lo ? (t_hi + 15) / 16 : b_lo;
+  const int nb = b_hi - b_lo > (int)blockIdx.x ? (b_hi - b_lo - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x : 0;
+  auto block_of = [&](int j) { return b_lo + (int)blockIdx.x + j * (int)gridDim.x; };
+  auto issue = [&](int j) {                        // one thread: block j into its stage
+    const int st = j % stages;
+    const uint32_t bar = smem_u32(&full[st]);
+    loads[st] = loads[st] + 1;
+    mbar_arrive_expect_tx(bar, (uint32_t)L.stage);
+    tma_load_3d(smem_u32(smem + L.x + st * L.stage), &tmap_x, 0, block_of(j) * 16, 0, bar);
+  };
+  if (tid == 0) {
+    for (int i = 0; i < kFuMaxStages; ++i) {
+      mbar_init(smem_u32(&full[i]), 1);
+      done[i] = 0;
+      loads[i] = 0;
+    }
+    for (int i = 0; i < kFuRouters; ++i) {
+      mbar_init(smem_u32(&dl_full[i]), 1);
+      mbar_init(smem_u32(&dl_empty[i]), kFuCols);
+    }
+    mbar_init(smem_u32(wbar), 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    mbar_arrive_expect_tx(smem_u32(wbar), (uint32_t)(E * D * 2));
+    for (int e = 0; e < E; ++e)
+      bulk_load(smem_u32(smem + L.wg + e * L.wg_stride), static_cast<const uint8_t*>(a.wg) + (size_t)e * D * 2, (uint32_t)(D * 2),
+                smem_u32(wbar));
+    for (int j = 0; j < stages && j < nb; ++j) issue(j);
+  }
+  for (int i = tid; i < (EP - E) * (D / 8); i += kFuThreads)   // rows of no expert
+    *reinterpret_cast<uint4*>(smem + L.wg + (E + i / (D / 8)) * L.wg_stride + (i % (D / 8)) * 16) = make_uint4(0u, 0u, 0u, 0u);
+  __syncthreads();
+  int* status = a.status;
+  if (w < kFuRouters) {
+    // ------------------------------------------------ router warps
+    const uint32_t wg = smem_u32(smem + L.wg);
+    uint8_t* slot = smem + L.dl + w * L.dl_slot;
+    float* dp = reinterpret_cast<float*>(smem + L.dp) + w * 16 * EP;
+    float db[NE][2];
+#pragma unroll
+    for (int nt = 0; nt < NE; ++nt) db[nt][0] = db[nt][1] = 0.f;
+    bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(wbar), 0, abort_flag, status, 420));
+    bool waited = false;
+    float aux = 0.f;
+    for (int j = w; j < nb && ok; j += kFuRouters) {
+      const int rb = block_of(j), st = j % stages, t0 = rb * 16 + g;
+      const GatesAhead gates = load_gates(a, rb);
+      const bool live[2] = {t0 >= t_lo && t0 < t_hi, t0 + 8 >= t_lo && t0 + 8 < t_hi};
+      RowPair<NE> l, C;
+      bool in[2];
+      if (waited) load_counts<NE>(a, live, t0, C, in);
+      ok = wait_issued(&loads[st], j / stages + 1, abort_flag, status, 427) &&
+           mbar_wait(smem_u32(&full[st]), (j / stages) & 1, abort_flag, status, 421);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const uint32_t xs = smem_u32(smem + L.x + st * L.stage);
+      float acc[NE][4 / NE][4];                    // independent sums, to be added
+#pragma unroll
+      for (int nt = 0; nt < NE; ++nt)
+#pragma unroll
+        for (int u = 0; u < 4 / NE; ++u)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) acc[nt][u][q] = 0.f;
+#pragma unroll 2
+      for (int box = 0; box < D / 64; ++box) {     // four k16 steps
+        uint32_t b[NE][4][2];
+        if (NE == 1) {
+          ldsm_x4(wg + lj * L.wg_stride + box * 128 + li * 16, b[0][0][0], b[0][0][1], b[0][1][0], b[0][1][1]);
+          ldsm_x4(wg + lj * L.wg_stride + box * 128 + 64 + li * 16, b[0][2][0], b[0][2][1], b[0][3][0], b[0][3][1]);
+        } else {
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            ldsm_x4(wg + ((li >> 1) * 8 + lj) * L.wg_stride + box * 128 + ks * 32 + (li & 1) * 16, b[0][ks][0], b[0][ks][1],
+                    b[NE - 1][ks][0], b[NE - 1][ks][1]);
+        }
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+          const int row = (li & 1) * 8 + lj, chunk = ks * 2 + (li >> 1);
+          uint32_t a0, a1, a2, a3;
+          ldsm_x4(xs + box * 2048 + row * 128 + ((chunk ^ (row & 7)) << 4), a0, a1, a2, a3);
+#pragma unroll
+          for (int nt = 0; nt < NE; ++nt) mma_16816<F16>(acc[nt][ks % (4 / NE)], a0, a1, a2, a3, b[nt][ks][0], b[nt][ks][1]);
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NE; ++nt)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            float v = acc[nt][0][2 * r + q];
+#pragma unroll
+            for (int u = 1; u < 4 / NE; ++u) v += acc[nt][u][2 * r + q];
+            l[r][nt][q] = v;
+          }
+      if (a.dgate) scatter_gates<EP>(a, gates, rb, t_lo, t_hi, dp);
+      if (!waited) {                               // from here on: what count wrote
+        grid_dependency_wait();
+        waited = true;
+        aux = a.aux_scale / (float)max(*a.live, 1);
+        load_counts<NE>(a, live, t0, C, in);
+      }
+      logits_to_dl<NE>(a, rb, dp, aux, C, in, l);
+#pragma unroll
+      for (int nt = 0; nt < NE; ++nt)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) db[nt][q] += l[0][nt][q] + l[1][nt][q];
+      uint4 fa[P::A], fw[P::T];
+      float4 scale;
+      dl_fragments<NE, F16>(l, fa, fw, scale);
+      const int use = j / kFuRouters;
+      if (use > 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&dl_empty[w]), (use - 1) & 1, abort_flag, status, 422));
+        if (!ok) break;
+      }
+      uint4* out = reinterpret_cast<uint4*>(slot) + lane;
+#pragma unroll
+      for (int i = 0; i < P::A; ++i) out[i * 32] = fa[i];
+#pragma unroll
+      for (int i = 0; i < P::T; ++i) out[(P::A + i) * 32] = fw[i];
+      if (F16 && c == 0) reinterpret_cast<float4*>(slot + (P::A + P::T) * 512)[g] = scale;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&dl_full[w]));
+    }
+    if (!waited) grid_dependency_wait();
+#pragma unroll
+    for (int nt = 0; nt < NE; ++nt)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        float sum = db[nt][q];
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (g == 0) a.db_part[((size_t)blockIdx.x * kFuRouters + w) * EP + nt * 8 + 2 * c + q] = sum;
+      }
+  } else {
+    // ------------------------------------------------ column warps
+    const int cw = w - kFuRouters, groups = D / 32;
+    const int g0 = cw * groups / kFuCols, g1 = (cw + 1) * groups / kFuCols;
+    uint32_t wb[kFuGroups][4][NE];                 // gate weight fragments of dx: rows e = 8h + 2c, + 1
+    const uint16_t* wg = static_cast<const uint16_t*>(a.wg);
+    float acc[kFuGroups][4][4];
+#pragma unroll
+    for (int gi = 0; gi < kFuGroups; ++gi)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[gi][j][q] = 0.f;
+#pragma unroll
+        for (int h = 0; h < NE; ++h) {
+          const int e = h * 8 + 2 * c, d = (g0 + gi) * 32 + 8 * (g >> 1) + 2 * j + (g & 1);
+          const uint32_t u = g0 + gi < g1 && e < E ? wg[(size_t)e * D + d] : 0u;
+          const uint32_t v = g0 + gi < g1 && e + 1 < E ? wg[(size_t)(e + 1) * D + d] : 0u;
+          wb[gi][j][h] = u | (v << 16);
+        }
+      }
+    uint16_t* dx = static_cast<uint16_t*>(a.dx) + g0 * 32 + 8 * c;
+    const int gmax = fused_groups(D);
+    const uint8_t* held = smem + L.old + cw * held_blocks * gmax * 1024 + lane * 16;
+    auto copy_old = [&](int j) {                   // what dx holds of block j, this lane's own pieces
+      if (add && j < nb) {
+        const int t0 = block_of(j) * 16 + g, t1 = t0 + 8;
+        const bool v0 = t0 >= t_lo && t0 < t_hi, v1 = t1 >= t_lo && t1 < t_hi;
+        const uint32_t dst = smem_u32(held) + (j & (held_blocks - 1)) * gmax * 1024;
+        for (int gi = 0; gi < g1 - g0; ++gi) {
+          cp16(dst + gi * 1024, dx + (v0 ? (size_t)t0 * D : 0) + gi * 32, v0);
+          cp16(dst + gi * 1024 + 512, dx + (v1 ? (size_t)t1 * D : 0) + gi * 32, v1);
+        }
+      }
+      cp_commit();
+    };
+    copy_old(0);
+    if (held_blocks == 2) copy_old(1);
+    bool ok = true;
+    for (int j = 0; j < nb; ++j) {
+      const int rb = block_of(j), st = j % stages, t0 = rb * 16 + g, t1 = t0 + 8;
+      const bool v0 = t0 >= t_lo && t0 < t_hi, v1 = t1 >= t_lo && t1 < t_hi;
+      const int r = j % kFuRouters;
+      ok = mbar_wait(smem_u32(&dl_full[r]), (j / kFuRouters) & 1, abort_flag, status, 423) &&
+           mbar_wait(smem_u32(&full[st]), (j / stages) & 1, abort_flag, status, 424);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const uint8_t* old = held + (add ? (j & (held_blocks - 1)) * gmax * 1024 : 0);
+      const uint32_t xs = smem_u32(smem + L.x + st * L.stage);
+      const uint8_t* slot = smem + L.dl + r * L.dl_slot;
+      uint4 A[P::A], At[P::T];
+#pragma unroll
+      for (int i = 0; i < P::A; ++i) A[i] = reinterpret_cast<const uint4*>(slot)[i * 32 + lane];
+#pragma unroll
+      for (int i = 0; i < P::T; ++i) At[i] = reinterpret_cast<const uint4*>(slot)[(P::A + i) * 32 + lane];
+      float4 inv = make_float4(1.f, 1.f, 1.f, 0.f);
+      if (F16) inv = reinterpret_cast<const float4*>(slot + (P::A + P::T) * 512)[g];
+      // rows of no sequence may hold anything: their x counts as zero (tokens 2c, 2c+1 and 2c+8, 2c+9)
+      const bool whole = rb * 16 >= t_lo && rb * 16 + 16 <= t_hi;
+      uint32_t k0 = 0xffffffffu, k1 = 0xffffffffu;
+      if (!whole) {
+        auto live = [&](int i) { return rb * 16 + i >= t_lo && rb * 16 + i < t_hi; };
+        k0 = (live(2 * c) ? 0xffffu : 0u) | (live(2 * c + 1) ? 0xffff0000u : 0u);
+        k1 = (live(2 * c + 8) ? 0xffffu : 0u) | (live(2 * c + 9) ? 0xffff0000u : 0u);
+      }
+#pragma unroll
+      for (int gi = 0; gi < kFuGroups; ++gi) {
+        if (g0 + gi < g1) {
+          // ---- dWg += dl^T x: two tiles of 8 columns at a time
+          const int col = (g0 + gi) * 32;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int t = (li & 1) * 8 + lj, chunk = ((col & 63) >> 3) + 2 * h + (li >> 1);
+            uint32_t b[2][2];
+            ldsm_x4_t(xs + (col >> 6) * 2048 + t * 128 + ((chunk ^ (t & 7)) << 4), b[0][0], b[0][1], b[1][0], b[1][1]);
+            if (!whole) {
+              b[0][0] &= k0; b[1][0] &= k0;
+              b[0][1] &= k1; b[1][1] &= k1;
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {          // the block's product, smallest part first, then one addition
+              float d4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int i = P::T - 1; i >= 0; --i) mma_16816<F16>(d4, At[i].x, At[i].y, At[i].z, At[i].w, b[q][0], b[q][1]);
+              float* s4 = acc[gi][2 * h + q];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) s4[k] = F16 ? fmaf(d4[k], inv.z, s4[k]) : s4[k] + d4[k];
+            }
+          }
+          // ---- dx (+)= dl Wg
+          if (a.dx) {
+            float o0[8], o1[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float d4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int i = 0; i < P::A; ++i) mma_16816<F16>(d4, A[i].x, A[i].y, A[i].z, A[i].w, wb[gi][k][0], wb[gi][k][NE - 1]);
+              o0[2 * k] = d4[0]; o0[2 * k + 1] = d4[1]; o1[2 * k] = d4[2]; o1[2 * k + 1] = d4[3];
+            }
+            uint32_t r0[4], r1[4];
+            uint4 h0 = make_uint4(0u, 0u, 0u, 0u), h1 = h0;
+            if (add) {
+              if (gi == 0) {
+                if (held_blocks == 2) cp_wait<1>();
+                else cp_wait<0>();
+              }
+              h0 = *reinterpret_cast<const uint4*>(old + gi * 1024);
+              h1 = *reinterpret_cast<const uint4*>(old + gi * 1024 + 512);
+            }
+            const uint32_t* q0 = reinterpret_cast<const uint32_t*>(&h0);
+            const uint32_t* q1 = reinterpret_cast<const uint32_t*>(&h1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 f0 = H::unpack(q0[i]), f1 = H::unpack(q1[i]);
+              r0[i] = H::pack(fmaf(o0[2 * i], inv.x, f0.x), fmaf(o0[2 * i + 1], inv.x, f0.y));
+              r1[i] = H::pack(fmaf(o1[2 * i], inv.y, f1.x), fmaf(o1[2 * i + 1], inv.y, f1.y));
+            }
+            if (v0) __stcs(reinterpret_cast<uint4*>(dx + (size_t)t0 * D + gi * 32), make_uint4(r0[0], r0[1], r0[2], r0[3]));
+            if (v1) __stcs(reinterpret_cast<uint4*>(dx + (size_t)t1 * D + gi * 32), make_uint4(r1[0], r1[1], r1[2], r1[3]));
+          }
+        }
+      }
+      copy_old(j + held_blocks);                   // this block's have been used
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&dl_empty[r]));
+        __threadfence_block();
+        if (atomicAdd(&done[st], 1) == kFuCols - 1) {   // the last to leave the stage
+          done[st] = 0;
+          if (j + stages < nb) {
+            fence_async_shared();
+            issue(j + stages);
+          }
+        }
+      }
+    }
+    cp_wait<0>();
+    // this block's part of dWg: expert rows g (and g + 8), columns 8k + 2c, + 1 of each group
+    float* part = a.partials + (size_t)blockIdx.x * E * D + 2 * c;
+#pragma unroll
+    for (int gi = 0; gi < kFuGroups; ++gi)
+      if (g0 + gi < g1) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float* s4 = acc[gi][k];
+          const int d = (g0 + gi) * 32 + 8 * k;
+          if (NE == 1) {
+            if (g < E) *reinterpret_cast<float2*>(part + (size_t)g * D + d) = make_float2(s4[0] + s4[2], s4[1] + s4[3]);
+          } else {
+            if (g < E) *reinterpret_cast<float2*>(part + (size_t)g * D + d) = make_float2(s4[0], s4[1]);
+            if (g + 8 < E) *reinterpret_cast<float2*>(part + (size_t)(g + 8) * D + d) = make_float2(s4[2], s4[3]);
+          }
+        }
+      }
+  }
+  // after a wait that ran out: no load may outlive the block
+  __syncthreads();
+  if (*abort_flag && tid == 0) {
+    for (int st = 0; st < stages; ++st)
+      if (loads[st]) mbar_wait(smem_u32(&full[st]), (loads[st] - 1) & 1, nullptr, nullptr, 425);
+    mbar_wait(smem_u32(wbar), 0, nullptr, nullptr, 426);
+  }
+}
+
 // ---------------------------------------------------------------- fp32
 // FFMA throughout (a tensor core would round x).  One warp per TOK tokens: lane l holds columns
 // 4l + 128 i of their rows and of Wg's.  TOK: four share each read of Wg where the tokens fill the
@@ -784,12 +1240,17 @@ __global__ void __launch_bounds__(kFinThreads) seq_finish_kernel(SeqBalArgs a, c
   if (blk < wg_blocks) {
     const int i = blk * 32 + lane;                 // E * D is a multiple of 64
     const size_t stride = (size_t)a.E * a.D;
-    float r[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int k = w; k < a.groups; k += NW * 8)
+    constexpr int kRound = 20;                     // 148 partial sums over 8 warps: all on their way at once
+    float sum = 0.f;
+    for (int k0 = w; k0 < a.groups; k0 += NW * kRound) {
+      float r[kRound];
 #pragma unroll
-      for (int u = 0; u < 8; ++u)
-        if (k + u * NW < a.groups) r[u] += __ldcg(a.partials + (size_t)(k + u * NW) * stride + i);
-    ws[w][lane] = ((r[0] + r[1]) + (r[2] + r[3])) + ((r[4] + r[5]) + (r[6] + r[7]));
+      for (int u = 0; u < kRound; ++u)
+        r[u] = k0 + u * NW < a.groups ? __ldcg(a.partials + (size_t)(k0 + u * NW) * stride + i) : 0.f;
+#pragma unroll
+      for (int u = 0; u < kRound; u += 4) sum += (r[u] + r[u + 1]) + (r[u + 2] + r[u + 3]);
+    }
+    ws[w][lane] = sum;
     __syncthreads();
     if (w == 0) {
       float t = 0.f;
@@ -855,6 +1316,15 @@ cudaError_t chained(void (*k)(P...), int grid, int threads, int smem, cudaStream
 template <int NE, bool F16>
 cudaError_t launch16(const SeqBalArgs& a, cudaStream_t s) {
   const int nblk = (a.T + 15) / 16;
+  if constexpr (NE <= 2) {
+    if (a.fused) {
+      using P = Parts<NE, F16>;
+      const bool add = a.dx && a.accumulate;
+      const FusedPlan f = fused_plan(a.D, NE, P::A + P::T, add);
+      return chained(seq_fused_kernel<NE, F16>, a.groups, kFuThreads,
+                     fused_smem(a.D, NE, P::A + P::T, f.stages, f.held).total, s, *a.tmap_x, a, f.stages, f.held);
+    }
+  }
   cudaError_t e = chained(seq_scores_kernel<NE, F16>, (nblk + kScWarps - 1) / kScWarps, kScWarps * 32, kScSmem, s, a);
   if (e != cudaSuccess || !a.grads) return e;
   return chained(seq_grads_kernel<NE, F16>, a.D / 64 * a.groups, 128, GradRing<NE, F16>::Smem, s, a);
@@ -883,7 +1353,18 @@ size_t seq_balance_frag_bytes(int E, int dtype) {
   return (size_t)n * 512;
 }
 
+bool seq_balance_fused(int D, int E, int dtype) {
+  if (dtype == MOE_F32 || E > 16 || D / 32 > kFuCols * kFuGroups) return false;
+  return fused_plan(D, E <= 8 ? 1 : 2, (int)(seq_balance_frag_bytes(E, dtype) / 512), true).stages >= 2;
+}
+
 void seq_balance_plan(int T, int D, int E, int dtype, int* groups, int* blocks_per_range) {
+  if (seq_balance_fused(D, E, dtype)) {     // one block an SM, token blocks in turn
+    const int nblk = (T + 15) / 16;
+    *groups = nblk < kSbSms ? nblk : kSbSms;
+    *blocks_per_range = 0;
+    return;
+  }
   const int slabs = dtype == MOE_F32 ? (D + 127) / 128 : D / 64;
   const int nblk = (T + 15) / 16;
   int r = kSbSms * (E <= 16 ? 3 : 2) / slabs * 4;  // one wave of blocks, four ranges each
@@ -896,16 +1377,17 @@ void seq_balance_plan(int T, int D, int E, int dtype, int* groups, int* blocks_p
 
 cudaError_t launch_seq_balance(const SeqBalArgs& a, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
-  const bool small = a.T <= kCountSmall && (long long)a.n_seqs * a.E <= kCountSmall && a.n_seqs < kOffSmem;
-  if (small) {
-    seq_count_kernel<true><<<1, 1024, 0, s>>>(a);
+  if (a.T <= kOneTokens && (long long)a.n_seqs * a.E <= kOneCounts && a.n_seqs < kOffSmem) {
+    seq_count_kernel<true><<<1, kOneThreads, 0, s>>>(a);
+    e = cudaGetLastError();
   } else {
     e = cudaMemsetAsync(a.counts, 0, (size_t)a.n_seqs * a.E * sizeof(int32_t), s);
     if (e == cudaSuccess && a.n_seqs >= kOffSmem) e = cudaMemsetAsync(a.live, 0, sizeof(int), s);
     if (e != cudaSuccess) return e;
     seq_count_kernel<false><<<(a.T + kCountThreads - 1) / kCountThreads, kCountThreads, 0, s>>>(a);
+    e = cudaGetLastError();
   }
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (e != cudaSuccess) return e;
   if (a.dtype == MOE_F32)
     e = a.E <= 8 ? launch32<8>(a, s) : a.E <= 16 ? launch32<16>(a, s) : launch32<32>(a, s);
   else
@@ -913,8 +1395,9 @@ cudaError_t launch_seq_balance(const SeqBalArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int wg_blocks = a.dwg ? a.E * a.D / 32 : 0, db_blocks = a.dbias ? a.E : 0;
   const bool f32 = a.dtype == MOE_F32;
+  const int db_rows = f32 ? a.T : a.fused ? a.groups * kFuRouters : (a.T + 15) / 16;
   return chained(seq_finish_kernel, wg_blocks + db_blocks + a.n_seqs + 1, kFinThreads, 0, s, a,
-                 (const float*)(f32 ? a.dl : a.db_part), f32 ? a.T : (a.T + 15) / 16, seq_balance_ep(a.E), wg_blocks, db_blocks);
+                 (const float*)(f32 ? a.dl : a.db_part), db_rows, seq_balance_ep(a.E), wg_blocks, db_blocks);
 }
 
 }  // namespace moe
