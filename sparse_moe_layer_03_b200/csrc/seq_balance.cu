@@ -669,15 +669,15 @@ __global__ void __launch_bounds__(128, NE == 4 ? 2 : 3) seq_grads_kernel(SeqBalA
 }
 
 // ---------------------------------------------------------------- scores and grads in one, 16-bit types
-// One block of 16 warps an SM over every grid-th 16-token block; x comes in once, by TMA, into a ring of
+// One block of 15 warps an SM over every grid-th 16-token block; x comes in once, by TMA, into a ring of
 // whole blocks of rows (64-column boxes, 128-byte swizzle) and leaves it when both halves are done:
-//   4 router warps, a token block each in turn: logits (ldmatrix and mma.sync on the stage), softmax, dl,
+//   3 router warps, a token block each in turn: logits (ldmatrix and mma.sync on the stage), softmax, dl,
 //     left in shared memory in fragment order;
 //   12 column warps, each a slice of 32-column groups over all the block's tokens: dWg in registers from
 //     the stage (transposed ldmatrix), dx from dl and the gate weight's columns in registers.
 // They meet on mbarriers only (dl full and empty by router, x full by stage); the last column warp to leave
 // a stage refills it.  For E <= 16 and rows of at most 1152.
-constexpr int kFuRouters = 4, kFuCols = 12, kFuThreads = (kFuRouters + kFuCols) * 32;
+constexpr int kFuRouters = 3, kFuCols = 12, kFuThreads = (kFuRouters + kFuCols) * 32;
 constexpr int kFuGroups = 3;                       // 32-column groups a column warp holds
 constexpr int kFuMaxStages = 6;
 constexpr int kFuMaxSmem = 232448;
@@ -937,9 +937,7 @@ seq_fused_kernel(const __grid_constant__ CUtensorMap tmap_x, const SeqBalArgs a,
       const uint8_t* old = held + (add ? (j & (held_blocks - 1)) * gmax * 1024 : 0);
       const uint32_t xs = smem_u32(smem + L.x + st * L.stage);
       const uint8_t* slot = smem + L.dl + r * L.dl_slot;
-      uint4 A[P::A], At[P::T];
-#pragma unroll
-      for (int i = 0; i < P::A; ++i) A[i] = reinterpret_cast<const uint4*>(slot)[i * 32 + lane];
+      uint4 At[P::T];
 #pragma unroll
       for (int i = 0; i < P::T; ++i) At[i] = reinterpret_cast<const uint4*>(slot)[(P::A + i) * 32 + lane];
       float4 inv = make_float4(1.f, 1.f, 1.f, 0.f);
@@ -976,8 +974,30 @@ seq_fused_kernel(const __grid_constant__ CUtensorMap tmap_x, const SeqBalArgs a,
               for (int k = 0; k < 4; ++k) s4[k] = F16 ? fmaf(d4[k], inv.z, s4[k]) : s4[k] + d4[k];
             }
           }
-          // ---- dx (+)= dl Wg
-          if (a.dx) {
+        }
+      }
+      // this warp is done with x: the last one to leave the stage refills it
+      __syncwarp();
+      if (lane == 0) {
+        __threadfence_block();
+        if (atomicAdd(&done[st], 1) == kFuCols - 1) {
+          done[st] = 0;
+          if (j + stages < nb) {
+            fence_async_shared();
+            issue(j + stages);
+          }
+        }
+      }
+      // ---- dx (+)= dl Wg
+      if (a.dx) {
+        uint4 A[P::A];
+#pragma unroll
+        for (int i = 0; i < P::A; ++i) A[i] = reinterpret_cast<const uint4*>(slot)[i * 32 + lane];
+        if (held_blocks == 2) cp_wait<1>();
+        else if (held_blocks == 1) cp_wait<0>();
+#pragma unroll
+        for (int gi = 0; gi < kFuGroups; ++gi) {
+          if (g0 + gi < g1) {
             float o0[8], o1[8];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -989,10 +1009,6 @@ seq_fused_kernel(const __grid_constant__ CUtensorMap tmap_x, const SeqBalArgs a,
             uint32_t r0[4], r1[4];
             uint4 h0 = make_uint4(0u, 0u, 0u, 0u), h1 = h0;
             if (add) {
-              if (gi == 0) {
-                if (held_blocks == 2) cp_wait<1>();
-                else cp_wait<0>();
-              }
               h0 = *reinterpret_cast<const uint4*>(old + gi * 1024);
               h1 = *reinterpret_cast<const uint4*>(old + gi * 1024 + 512);
             }
@@ -1011,17 +1027,7 @@ seq_fused_kernel(const __grid_constant__ CUtensorMap tmap_x, const SeqBalArgs a,
       }
       copy_old(j + held_blocks);                   // this block's have been used
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(smem_u32(&dl_empty[r]));
-        __threadfence_block();
-        if (atomicAdd(&done[st], 1) == kFuCols - 1) {   // the last to leave the stage
-          done[st] = 0;
-          if (j + stages < nb) {
-            fence_async_shared();
-            issue(j + stages);
-          }
-        }
-      }
+      if (lane == 0) mbar_arrive(smem_u32(&dl_empty[r]));
     }
     cp_wait<0>();
     // this block's part of dWg: expert rows g (and g + 8), columns 8k + 2c, + 1 of each group
