@@ -751,18 +751,6 @@ seq_fused_kernel(const __grid_constant__ CUtensorMap tmap_x, const SeqBalArgs a,
   volatile int* loads = done + kFuMaxStages;       // loads issued into a stage
   volatile int* abort_flag = loads + kFuMaxStages;
   launch_dependents();
-  int t_lo, t_hi;
-  live_rows(a, t_lo, t_hi);
-  const int b_lo = t_lo / 16, b_hi = t_hi > t_lo ? (t_hi + 15) / 16 : b_lo;
-  const int nb = b_hi - b_lo > (int)blockIdx.x ? (b_hi - b_lo - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x : 0;
-  auto block_of = [&](int j) { return b_lo + (int)blockIdx.x + j * (int)gridDim.x; };
-  auto issue = [&](int j) {                        // one thread: block j into its stage
-    const int st = j % stages;
-    const uint32_t bar = smem_u32(&full[st]);
-    loads[st] = loads[st] + 1;
-    mbar_arrive_expect_tx(bar, (uint32_t)L.stage);
-    tma_load_3d(smem_u32(smem + L.x + st * L.stage), &tmap_x, 0, block_of(j) * 16, 0, bar);
-  };
   if (tid == 0) {
     for (int i = 0; i < kFuMaxStages; ++i) {
       mbar_init(smem_u32(&full[i]), 1);
@@ -780,8 +768,21 @@ seq_fused_kernel(const __grid_constant__ CUtensorMap tmap_x, const SeqBalArgs a,
     for (int e = 0; e < E; ++e)
       bulk_load(smem_u32(smem + L.wg + e * L.wg_stride), static_cast<const uint8_t*>(a.wg) + (size_t)e * D * 2, (uint32_t)(D * 2),
                 smem_u32(wbar));
-    for (int j = 0; j < stages && j < nb; ++j) issue(j);
   }
+  int t_lo, t_hi;
+  live_rows(a, t_lo, t_hi);
+  const int b_lo = t_lo / 16, b_hi = t_hi > t_lo ? (t_hi + 15) / 16 : b_lo;
+  const int nb = b_hi - b_lo > (int)blockIdx.x ? (b_hi - b_lo - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x : 0;
+  auto block_of = [&](int j) { return b_lo + (int)blockIdx.x + j * (int)gridDim.x; };
+  auto issue = [&](int j) {                        // one thread: block j into its stage
+    const int st = j % stages;
+    const uint32_t bar = smem_u32(&full[st]);
+    loads[st] = loads[st] + 1;
+    mbar_arrive_expect_tx(bar, (uint32_t)L.stage);
+    tma_load_3d(smem_u32(smem + L.x + st * L.stage), &tmap_x, 0, block_of(j) * 16, 0, bar);
+  };
+  if (tid == 0)
+    for (int j = 0; j < stages && j < nb; ++j) issue(j);
   for (int i = tid; i < (EP - E) * (D / 8); i += kFuThreads)   // rows of no expert
     *reinterpret_cast<uint4*>(smem + L.wg + (E + i / (D / 8)) * L.wg_stride + (i % (D / 8)) * 16) = make_uint4(0u, 0u, 0u, 0u);
   __syncthreads();
@@ -1069,6 +1070,16 @@ __global__ void __launch_bounds__(128) seq_scores_f32_kernel(SeqBalArgs a) {
   launch_dependents();
   int t_lo, t_hi;
   live_rows(a, t_lo, t_hi);
+  // the tokens' gate gradients, lane k holding slot k (at most 32 experts), on their way meanwhile
+  int slots[TOK], sel[TOK];
+  float gate[TOK];
+#pragma unroll
+  for (int i = 0; i < TOK; ++i) {
+    const bool in = a.dgate && tb + i < a.T;
+    slots[i] = in ? slots_of(a, tb + i) : 0;
+    sel[i] = in && lane < a.Kmax ? a.topk_idx[(size_t)(tb + i) * a.Kmax + lane] : -1;
+    gate[i] = in && lane < a.Kmax ? a.dgate[(size_t)(tb + i) * a.Kmax + lane] : 0.f;
+  }
   float l[TOK][EP];
 #pragma unroll
   for (int i = 0; i < TOK; ++i)
@@ -1102,16 +1113,24 @@ __global__ void __launch_bounds__(128) seq_scores_f32_kernel(SeqBalArgs a) {
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], o);
   // every lane holds every sum; lane e keeps expert e's
+  const float bias = lane < E && a.bias ? a.bias[lane] : 0.f;
   grid_dependency_wait();
   const float aux = a.aux_scale / (float)max(*a.live, 1);
+  int2 tok[TOK];
+  float C[TOK];
+#pragma unroll
+  for (int i = 0; i < TOK; ++i) tok[i] = tb + i >= t_lo && tb + i < t_hi ? a.tok[tb + i] : make_int2(-1, 0);
+#pragma unroll
+  for (int i = 0; i < TOK; ++i)
+    C[i] = tok[i].x >= 0 && lane < E ? __int_as_float(tok[i].y) * (float)a.counts[(size_t)tok[i].x * E + lane] : 0.f;
 #pragma unroll
   for (int i = 0; i < TOK; ++i) {
     const int t = tb + i;
+    const int2 tk = tok[i];
     float mine = -INFINITY;
 #pragma unroll
     for (int e = 0; e < EP; ++e)
-      if (lane == e && e < E) mine = l[i][e] + (a.bias ? a.bias[e] : 0.f);
-    const int2 tk = t >= t_lo && t < t_hi ? a.tok[t] : make_int2(-1, 0);
+      if (lane == e && e < E) mine = l[i][e] + bias;
     float m = mine;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -1120,14 +1139,14 @@ __global__ void __launch_bounds__(128) seq_scores_f32_kernel(SeqBalArgs a) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
     const float P = pe * (1.0f / z);
-    const float C = tk.x >= 0 && lane < E ? __int_as_float(tk.y) * (float)a.counts[(size_t)tk.x * E + lane] : 0.f;
-    float dp = aux * C;
-    if (a.dgate && tk.x >= 0) {
-      const int ns = slots_of(a, t);
-      for (int k = 0; k < ns; ++k)
-        if (a.topk_idx[(size_t)t * a.Kmax + k] == lane) dp += a.dgate[(size_t)t * a.Kmax + k];
+    float dp = aux * C[i];
+    const int ns = tk.x >= 0 ? slots[i] : 0;       // the same in every lane
+    for (int k = 0; k < ns; ++k) {
+      const int e = __shfl_sync(0xffffffffu, sel[i], k);
+      const float v = __shfl_sync(0xffffffffu, gate[i], k);
+      if (e == lane) dp += v;
     }
-    float share = P * C, pc = P * dp;
+    float share = P * C[i], pc = P * dp;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       share += __shfl_xor_sync(0xffffffffu, share, o);
@@ -1140,7 +1159,8 @@ __global__ void __launch_bounds__(128) seq_scores_f32_kernel(SeqBalArgs a) {
   }
 }
 
-// One block per (128 columns, four ranges of 16-token blocks), a warp to a range: lane l owns four
+constexpr int kF32Unit = 4;                        // ranges are a multiple of this many tokens
+// One block per (128 columns, four ranges of tokens), a warp to a range: lane l owns four
 // columns, its slice of dWg in registers over the range.  D is a multiple of 64: half of a last slab
 // may idle.  Four tokens' rows are loaded together.  Wg's columns stay in registers up to 8 experts.
 template <int EP>
@@ -1155,8 +1175,8 @@ __global__ void __launch_bounds__(128) seq_grads_f32_kernel(SeqBalArgs a) {
   const int range = group * 4 + w;
   int t_lo, t_hi;
   live_rows(a, t_lo, t_hi);
-  const int t_begin = max(range * a.blocks_per_range * 16, t_lo);
-  const int t_end = min(min(a.T, t_hi), (range + 1) * a.blocks_per_range * 16);
+  const int t_begin = max(range * a.blocks_per_range * kF32Unit, t_lo);
+  const int t_end = min(min(a.T, t_hi), (range + 1) * a.blocks_per_range * kF32Unit);
   float4 acc[EP], wv[EP == 8 ? EP : 1];
   const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
   const float* x = static_cast<const float*>(a.x) + col;
@@ -1371,8 +1391,8 @@ void seq_balance_plan(int T, int D, int E, int dtype, int* groups, int* blocks_p
     *blocks_per_range = 0;
     return;
   }
-  const int slabs = dtype == MOE_F32 ? (D + 127) / 128 : D / 64;
-  const int nblk = (T + 15) / 16;
+  const int slabs = dtype == MOE_F32 ? (D + 127) / 128 : D / 64, unit = dtype == MOE_F32 ? kF32Unit : 16;
+  const int nblk = (T + unit - 1) / unit;
   int r = kSbSms * (E <= 16 ? 3 : 2) / slabs * 4;  // one wave of blocks, four ranges each
   if (r > nblk) r = nblk;
   if (r < 1) r = 1;
