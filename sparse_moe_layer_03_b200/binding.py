@@ -147,11 +147,7 @@ def header_symbols(path: str = HEADER) -> list:
 
 
 def _ptr(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    return t if t is None or type(t) is int else t.data_ptr()
 
 
 def _check(rc: int):

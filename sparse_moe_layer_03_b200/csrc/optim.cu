@@ -122,6 +122,7 @@ template <int CAP>
 __global__ void __launch_bounds__(kOptThreads) grad_norm_kernel(const __grid_constant__ NormParams<CAP> a) {
   __shared__ double sh[kOptThreads / 32];
   __shared__ int is_last;
+  launch_dependents();                             // the step's kernel, if it comes next, is set up meanwhile
   double s = 0.0;
   for (int chunk = blockIdx.x; chunk < a.chunks; chunk += gridDim.x) {
     const int k = find_tensor(a.chunk_end, a.tensors, chunk);
@@ -259,6 +260,7 @@ template <bool Q8, int CAP>
 __global__ void __launch_bounds__(kOptThreads, kOptPerSm) adamw_kernel(const __grid_constant__ AdamwParams<CAP> a) {
   __shared__ StepScalars ss;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  grid_dependency_wait();                          // a programmatic dependent of what runs before (the norm)
   if (tid == 0) {
     const OptCtl& c = *a.ctl;
     const double c1 = 1.0 - c.beta1_t * a.beta1, c2 = 1.0 - c.beta2_t * a.beta2;
@@ -515,8 +517,16 @@ cudaError_t adamw_launch(const moe_adamw_t& h, const moe_adamw_tensor_t* t, int 
   a.ctl = ctl;
   const long long most = (long long)sms * kOptPerSm;   // one wave
   const int grid = (int)(chunks < 1 ? 1 : chunks < most ? chunks : most);
-  adamw_kernel<Q8, CAP><<<grid, kOptThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kOptThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, adamw_kernel<Q8, CAP>, a);
 }
 
 template <bool Q8>

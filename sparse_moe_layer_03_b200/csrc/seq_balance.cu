@@ -28,6 +28,8 @@
 // 16-bit parts that add up to it: for dx two; for dWg, which stays in fp32, three of bf16 (24 bits)
 // or two of fp16 (22 bits below the largest of its 16 tokens; each row of dx has a scale of its own).
 // With E <= 8 two parts share one k16 step.
+#include <atomic>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -1320,11 +1322,20 @@ __global__ void __launch_bounds__(kFinThreads) seq_finish_kernel(SeqBalArgs a, c
   }
 }
 
-template <typename... P, typename... Q>
-cudaError_t chained(void (*k)(P...), int grid, int threads, int smem, cudaStream_t s, Q... args) {
-  if (smem > 32 * 1024) {                          // with what a kernel declares, above the default 48 KB
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+// Launch K as a programmatic dependent of the kernel before.  Its limit of dynamic shared memory, MOST, is
+// raised once on each device.
+template <auto K, int MOST, typename... Q>
+cudaError_t chained(int grid, int threads, int smem, cudaStream_t s, const Q&... args) {
+  if (MOST > 32 * 1024) {                          // with what a kernel declares, above the default 48 KB
+    static std::atomic<unsigned long long> raised{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+    if (!(raised.load(std::memory_order_relaxed) & bit)) {
+      if ((e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, MOST)) != cudaSuccess) return e;
+      raised.fetch_or(bit, std::memory_order_relaxed);
+    }
   }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)grid);
@@ -1336,7 +1347,7 @@ cudaError_t chained(void (*k)(P...), int grid, int threads, int smem, cudaStream
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k, args...);
+  return cudaLaunchKernelEx(&cfg, K, args...);
 }
 
 template <int NE, bool F16>
@@ -1347,20 +1358,20 @@ cudaError_t launch16(const SeqBalArgs& a, cudaStream_t s) {
       using P = Parts<NE, F16>;
       const bool add = a.dx && a.accumulate;
       const FusedPlan f = fused_plan(a.D, NE, P::A + P::T, add);
-      return chained(seq_fused_kernel<NE, F16>, a.groups, kFuThreads,
+      return chained<seq_fused_kernel<NE, F16>, kFuMaxSmem>(a.groups, kFuThreads,
                      fused_smem(a.D, NE, P::A + P::T, f.stages, f.held).total, s, *a.tmap_x, a, f.stages, f.held);
     }
   }
-  cudaError_t e = chained(seq_scores_kernel<NE, F16>, (nblk + kScWarps - 1) / kScWarps, kScWarps * 32, kScSmem, s, a);
+  cudaError_t e = chained<seq_scores_kernel<NE, F16>, kScSmem>((nblk + kScWarps - 1) / kScWarps, kScWarps * 32, kScSmem, s, a);
   if (e != cudaSuccess || !a.grads) return e;
-  return chained(seq_grads_kernel<NE, F16>, a.D / 64 * a.groups, 128, GradRing<NE, F16>::Smem, s, a);
+  return chained<seq_grads_kernel<NE, F16>, GradRing<NE, F16>::Smem>(a.D / 64 * a.groups, 128, GradRing<NE, F16>::Smem, s, a);
 }
 template <int EP>
 cudaError_t launch32(const SeqBalArgs& a, cudaStream_t s) {
-  cudaError_t e = a.T <= kSbF32Single ? chained(seq_scores_f32_kernel<EP, 1>, (a.T + 3) / 4, 128, 0, s, a)
-                                      : chained(seq_scores_f32_kernel<EP, 4>, (a.T + 15) / 16, 128, 0, s, a);
+  cudaError_t e = a.T <= kSbF32Single ? chained<seq_scores_f32_kernel<EP, 1>, 0>((a.T + 3) / 4, 128, 0, s, a)
+                                      : chained<seq_scores_f32_kernel<EP, 4>, 0>((a.T + 15) / 16, 128, 0, s, a);
   if (e != cudaSuccess || !a.grads) return e;
-  return chained(seq_grads_f32_kernel<EP>, (a.D + 127) / 128 * a.groups, 128, EP * 2048, s, a);
+  return chained<seq_grads_f32_kernel<EP>, EP * 2048>((a.D + 127) / 128 * a.groups, 128, EP * 2048, s, a);
 }
 template <bool F16>
 cudaError_t launch16_e(const SeqBalArgs& a, cudaStream_t s) {
@@ -1422,7 +1433,7 @@ cudaError_t launch_seq_balance(const SeqBalArgs& a, cudaStream_t s) {
   const int wg_blocks = a.dwg ? a.E * a.D / 32 : 0, db_blocks = a.dbias ? a.E : 0;
   const bool f32 = a.dtype == MOE_F32;
   const int db_rows = f32 ? a.T : a.fused ? a.groups * kFuRouters : (a.T + 15) / 16;
-  return chained(seq_finish_kernel, wg_blocks + db_blocks + a.n_seqs + 1, kFinThreads, 0, s, a,
+  return chained<seq_finish_kernel, 0>(wg_blocks + db_blocks + a.n_seqs + 1, kFinThreads, 0, s, a,
                  (const float*)(f32 ? a.dl : a.db_part), db_rows, seq_balance_ep(a.E), wg_blocks, db_blocks);
 }
 
