@@ -1166,6 +1166,7 @@ int moe_seq_balance(const moe_config_t* cfg, const void* x, const void* wg, cons
     return fail(MOE_ERR_INVALID_ARG, "n_seqs=%d images of %d tokens are not T=%d", n_seqs, seq_len, cfg->T);
   if (!dwg && (dbias || dx || dgate)) return fail(MOE_ERR_INVALID_ARG, "dbias, dx and dgate need dwg");
   if (dx_accumulate && !dx) return fail(MOE_ERR_INVALID_ARG, "dx_accumulate needs dx");
+  if (dx && dx == x) return fail(MOE_ERR_INVALID_ARG, "dx and x are one buffer");
   if (!std::isfinite(aux_scale)) return fail(MOE_ERR_INVALID_ARG, "aux_scale=%g", aux_scale);
   if (cfg->routing == MOE_ROUTE_RACE && !n_sel) return fail(MOE_ERR_INVALID_ARG, "n_sel is required for Expert-Race routing");
   if (n_seqs > 0) {

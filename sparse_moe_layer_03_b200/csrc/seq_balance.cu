@@ -67,6 +67,15 @@ __device__ __forceinline__ int slots_of(const SeqBalArgs& a, int t) {
 }
 
 // ---------------------------------------------------------------- count
+// Counts (and the number of sequences that hold a row) to zero, ahead of the count kernel, which is set up
+// and has found its tokens' sequences by the time it ends (a memset would be waited for).
+__global__ void __launch_bounds__(kCountThreads) seq_clear_kernel(int32_t* counts, long long n, int* live) {
+  launch_dependents();
+  for (long long i = (long long)blockIdx.x * kCountThreads + threadIdx.x; i < n; i += (long long)gridDim.x * kCountThreads)
+    counts[i] = 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *live = 0;
+}
+
 // One thread per token: its sequence by binary search, its selected experts into the counts.  ONE: one
 // block, the counts in shared memory; no clearing, no global atomics.  Else equal (sequence, expert) keys of
 // a warp are merged (as in the frequency kernel) and added to counts that were cleared before.  The choice
@@ -104,6 +113,7 @@ __global__ void __launch_bounds__(ONE ? kOneThreads : kCountThreads) seq_count_k
   };
   load_slots(blockIdx.x * nt + tid);
   __syncthreads();
+  if (!ONE) grid_dependency_wait();                // the counts are clear
   // sequences that hold a row: by the first block where it has the offsets at hand, else by all blocks
   if (off && (!in_smem || blockIdx.x == 0)) {
     int full = 0;
@@ -1418,11 +1428,11 @@ cudaError_t launch_seq_balance(const SeqBalArgs& a, cudaStream_t s) {
     seq_count_kernel<true><<<1, kOneThreads, 0, s>>>(a);
     e = cudaGetLastError();
   } else {
-    e = cudaMemsetAsync(a.counts, 0, (size_t)a.n_seqs * a.E * sizeof(int32_t), s);
-    if (e == cudaSuccess && a.n_seqs >= kOffSmem) e = cudaMemsetAsync(a.live, 0, sizeof(int), s);
-    if (e != cudaSuccess) return e;
-    seq_count_kernel<false><<<(a.T + kCountThreads - 1) / kCountThreads, kCountThreads, 0, s>>>(a);
-    e = cudaGetLastError();
+    const long long counts = (long long)a.n_seqs * a.E;
+    const int clear = (int)(counts < 256 * kCountThreads ? (counts + kCountThreads - 1) / kCountThreads : 256);
+    seq_clear_kernel<<<clear > 0 ? clear : 1, kCountThreads, 0, s>>>(a.counts, counts, a.live);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = chained<seq_count_kernel<false>, 0>((a.T + kCountThreads - 1) / kCountThreads, kCountThreads, 0, s, a);
   }
   if (e != cudaSuccess) return e;
   if (a.dtype == MOE_F32)

@@ -278,6 +278,53 @@ def test_bad_offsets_and_experts_are_reported():
         c.run()
 
 
+@pytest.mark.parametrize("dt", list(TYPES))
+def test_no_sequences(dt):
+    c = Case(40, 64, 4, 2, dt, offsets=[0, 40])
+    c.offsets, c.n = [0], 0
+    c.live[:] = False
+    o = c.run()
+    assert float(o["loss"]) == 0.0 and torch.count_nonzero(o["dwg"]) == 0 and torch.count_nonzero(o["dbias"]) == 0
+    assert np.array_equal(o["dx"].double().cpu().numpy(), O.as_f64(c.old))
+
+
+@pytest.mark.parametrize("E,dt", [(8, "bf16"), (32, "bf16"), (16, "f16"), (8, "f32")])
+def test_the_most_tokens_a_call_takes(E, dt):
+    # 262144 tokens of one sequence, and of 4096: against fp64 on the device (the CPU oracle's sums take
+    # minutes).  Normwise: dl is good to 1e-5 of its largest (logits of 64 products), sums of 2^18 rounded
+    # terms in fp32 to 2^18 u / 100 at the very worst order, u = 2^-24
+    T, D, K = 262144, 64, 2
+    g = torch.Generator(device=DEV).manual_seed(E)
+    rn = lambda *s: torch.randn(s, generator=g, device=DEV)  # noqa: E731
+    x, wg = rn(T, D).to(TYPES[dt]), (rn(E, D) / 8).to(TYPES[dt])
+    P = torch.softmax(x.double() @ wg.double().t(), 1)
+    idx = P.topk(K, 1).indices.to(torch.int32)
+    for n in (1, 4096):
+        off = torch.arange(n + 1, dtype=torch.int32, device=DEV) * (T // n)
+        cfg = B.make_config(T, D, 64, E, K, 0, dt, alpha=ALPHA)
+        nb = B.moe_seq_balance_workspace_size(cfg, n)
+        bws, st = torch.empty(nb, dtype=torch.uint8, device=DEV), torch.zeros(256, dtype=torch.uint8, device=DEV)
+        counts = torch.empty((n, E), dtype=torch.int32, device=DEV)
+        f = lambda *s: torch.empty(s, device=DEV)  # noqa: E731
+        per, loss, dwg, db, dx = f(n), f(1), f(E, D), f(E), torch.empty_like(x)
+        B.moe_seq_balance(cfg, x, wg, None, off, n, idx, None, None, 1e6, counts, per, loss, dwg, db, dx, 0, bws, nb, st,
+                          torch.cuda.current_stream().cuda_stream)
+        B.moe_check_status(st, torch.cuda.current_stream().cuda_stream)
+        sel = torch.zeros((T, E), dtype=torch.float64, device=DEV).scatter_(1, idx.long(), 1.0).view(n, T // n, E)
+        want = sel.sum(1)
+        assert torch.equal(counts, want.to(torch.int32))
+        C = (ALPHA * E / (K * (T // n) ** 2) * want)[:, None].expand(n, T // n, E).reshape(T, E)
+        assert torch.allclose(per.double(), (P * C).sum(1).view(n, -1).sum(1), rtol=2e-5)
+        assert abs(float(loss) - float((P * C).sum() / n)) <= 2e-5 * float(loss)
+        dP = 1e6 * C / n
+        dl = P * (dP - (P * dP).sum(1, keepdim=True))
+        for got, ref in ((dwg, dl.t() @ x.double()), (db, dl.sum(0))):
+            scale = float((dl.abs().t() @ x.double().abs()).max()) if ref.dim() == 2 else float(dl.abs().sum(0).max())
+            assert float((got.double() - ref).abs().max()) <= 2e-4 * scale
+        ref = dl @ wg.double()
+        assert float((dx.double() - ref).abs().max()) <= (HALF[dt] + 3e-5) * float(ref.abs().max()) + TINY[dt]
+
+
 def test_no_tokens():
     cfg = B.make_config(0, 128, 64, 4, 2, 0)
     nb = B.moe_seq_balance_workspace_size(cfg, 2)

@@ -82,7 +82,7 @@ def test_arguments_are_refused_before_a_launch():
              (cfg, dict(ws=None), b"ws"), (cfg, dict(x=None), b"x"), (cfg, dict(x=FAKE + 2), b"x"), (cfg, dict(wg=None), b"wg"),
              (cfg, dict(idx=None), b"topk_idx"), (cfg, dict(bias=FAKE + 4), b"router_bias"),
              (cfg, dict(off=FAKE + 4), b"seq_offsets"), (cfg, dict(dgate=FAKE + 4), b"dgate"),
-             (cfg, dict(n_sel=FAKE + 4), b"n_sel"), (cfg, dict(dx=FAKE + 8), b"dx")]
+             (cfg, dict(n_sel=FAKE + 4), b"n_sel"), (cfg, dict(dx=FAKE + 8), b"dx"), (cfg, dict(dx=FAKE), b"one buffer")]
     for c, kw, word in cases:
         assert _call(c, **kw) == B.MOE_ERR_INVALID_ARG, kw
         assert word in B.lib.moe_last_error(), (kw, B.lib.moe_last_error())
