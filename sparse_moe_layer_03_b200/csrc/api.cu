@@ -1133,12 +1133,12 @@ static SbLayout sb_layout(const moe_config_t* c) {
   L.live = take(256);
   L.tok = take(T * 8);
   L.tok_loss = take(T * 4);
-  L.blk_loss = take(is16(c) ? nblk * 4 : 0);
+  L.blk_loss = take(nblk * 4);
   L.frag = take(is16(c) ? nblk * seq_balance_frag_bytes(c->E, c->dtype) : 0);
   L.scales = take(c->dtype == MOE_F16 ? nblk * 128 : 0);
   L.dl = take(is16(c) ? 0 : T * ep * 4);
   // rows of the two kernels' token blocks, or four router warps of each block of the fused one
-  L.db_part = take(is16(c) ? (nblk > 4 * (size_t)groups ? nblk : 4 * (size_t)groups) * ep * 4 : 0);
+  L.db_part = take((nblk > 4 * (size_t)groups ? nblk : 4 * (size_t)groups) * ep * 4);
   L.partials = take((size_t)groups * c->E * c->D * 4);
   L.total = off;
   return L;
@@ -1210,7 +1210,7 @@ int moe_seq_balance(const moe_config_t* cfg, const void* x, const void* wg, cons
   a.live = ws_at<int>(bws, L.live);
   a.tok = ws_at<int2>(bws, L.tok);
   a.tok_loss = ws_at<float>(bws, L.tok_loss);
-  a.blk_loss = is16(cfg) ? ws_at<float>(bws, L.blk_loss) : nullptr;
+  a.blk_loss = cfg->dtype != MOE_F32 || cfg->T > kSbF32Single ? ws_at<float>(bws, L.blk_loss) : nullptr;
   a.frag = ws_at<uint4>(bws, L.frag);
   a.scales = ws_at<float4>(bws, L.scales);
   a.dl = ws_at<float>(bws, L.dl);

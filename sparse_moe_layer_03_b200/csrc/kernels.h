@@ -295,11 +295,11 @@ struct SeqBalArgs {
   int2* tok;                                          // [T] sequence (-1: none) and factor of its counts
   int* live;                                          // [1] sequences with a row
   float* tok_loss;                                    // [T]
-  float* blk_loss;                                    // 16-bit: [blocks] sums of 16 of them, else null
+  float* blk_loss;                                    // [blocks] sums of 16 of them, or null (fp32, few tokens)
   uint4* frag;                                        // 16-bit: dl in fragment order, seq_balance_frag_bytes a block
   float4* scales;                                     // fp16: [blocks, 8] inverse scales of rows g, g + 8 and the block
   float* dl;                                          // fp32: [T, ep]
-  float* db_part;                                     // 16-bit: [blocks, ep]
+  float* db_part;                                     // [blocks, ep] sums of dl over blocks of tokens
   float* partials;                                    // [groups, E, D]
   int* status;
 };

@@ -688,9 +688,12 @@ __global__ void __launch_bounds__(128, NE == 4 ? 2 : 3) seq_grads_kernel(SeqBalA
 //   12 column warps, each a slice of 32-column groups over all the block's tokens: dWg in registers from
 //     the stage (transposed ldmatrix), dx from dl and the gate weight's columns in registers.
 // They meet on mbarriers only (dl full and empty by router, x full by stage); the last column warp to leave
-// a stage refills it.  For E <= 16 and rows of at most 1152.
+// a stage refills it.  For E <= 16 and rows of 512 (narrower ones leave the column warps too little: the two
+// kernels' many independent warps hide latency better) to 1152.
 constexpr int kFuRouters = 3, kFuCols = 12, kFuThreads = (kFuRouters + kFuCols) * 32;
 constexpr int kFuGroups = 3;                       // 32-column groups a column warp holds
+constexpr int kFuMinD = 512;                       // bf16, E = 8, T = 32768: 41.0 us against the two kernels' 39.6 at D = 512,
+                                                   // 45.1 against 52.4 at 768; 34.9 against 24.7 at 256
 constexpr int kFuMaxStages = 6;
 constexpr int kFuMaxSmem = 232448;
 
@@ -1071,14 +1074,23 @@ seq_fused_kernel(const __grid_constant__ CUtensorMap tmap_x, const SeqBalArgs a,
 }
 
 // ---------------------------------------------------------------- fp32
+// x goes by L1, which keeps the gate weight that every token takes
+__device__ __forceinline__ float4 ld_past_l1(const float* p) {
+  float4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+  return v;
+}
 // FFMA throughout (a tensor core would round x).  One warp per TOK tokens: lane l holds columns
-// 4l + 128 i of their rows and of Wg's.  TOK: four share each read of Wg where the tokens fill the
-// device all the same, else one (T = 512: 18 us with four).
+// 4l + 128 i of their rows and of Wg's.  TOK: one where the tokens do not fill the device, else as many
+// share each read of Wg as registers hold: four with up to 8 experts (T = 32768, D = 1152, loss alone:
+// 70 us, two: 84), two above (32 experts, T = 8192: 83 us, four: 145).
 template <int EP, int TOK>
-__global__ void __launch_bounds__(128) seq_scores_f32_kernel(SeqBalArgs a) {
+__global__ void __launch_bounds__(TOK == 2 ? 256 : 128) seq_scores_f32_kernel(SeqBalArgs a) {
+  constexpr int NW = TOK == 2 ? 8 : 4;           // but for TOK = 1, 16 tokens a block
+  __shared__ float db_s[NW][EP], loss_s[NW];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int D = a.D, E = a.E;
-  const int tb = (blockIdx.x * 4 + w) * TOK;
+  const int tb = (blockIdx.x * NW + w) * TOK;
   launch_dependents();
   int t_lo, t_hi;
   live_rows(a, t_lo, t_hi);
@@ -1106,7 +1118,7 @@ __global__ void __launch_bounds__(128) seq_scores_f32_kernel(SeqBalArgs a) {
 #pragma unroll
     for (int i = 0; i < TOK; ++i) {
       const int t = tb + i;
-      xv[i] = t < a.T ? __ldg(reinterpret_cast<const float4*>(x + (size_t)t * D + d)) : zero;
+      xv[i] = t < a.T ? ld_past_l1(x + (size_t)t * D + d) : zero;
     }
 #pragma unroll
     for (int e = 0; e < EP; ++e) {
@@ -1130,6 +1142,7 @@ __global__ void __launch_bounds__(128) seq_scores_f32_kernel(SeqBalArgs a) {
   const float aux = a.aux_scale / (float)max(*a.live, 1);
   int2 tok[TOK];
   float C[TOK];
+  float db = 0.f, loss_w = 0.f;
 #pragma unroll
   for (int i = 0; i < TOK; ++i) tok[i] = tb + i >= t_lo && tb + i < t_hi ? a.tok[tb + i] : make_int2(-1, 0);
 #pragma unroll
@@ -1164,10 +1177,30 @@ __global__ void __launch_bounds__(128) seq_scores_f32_kernel(SeqBalArgs a) {
       share += __shfl_xor_sync(0xffffffffu, share, o);
       pc += __shfl_xor_sync(0xffffffffu, pc, o);
     }
+    share = tk.x >= 0 ? share : 0.f;
+    const float dl = tk.x >= 0 && lane < E ? P * (dp - pc) : 0.f;
     if (t < a.T) {
-      if (lane == 0) a.tok_loss[t] = tk.x >= 0 ? share : 0.f;
-      if (a.grads && lane < EP) a.dl[(size_t)t * EP + lane] = tk.x >= 0 && lane < E ? P * (dp - pc) : 0.f;
+      if (lane == 0) a.tok_loss[t] = share;
+      if (a.grads && lane < EP) a.dl[(size_t)t * EP + lane] = dl;
     }
+    db += dl;
+    loss_w += share;
+  }
+  if (TOK == 1) return;                            // few tokens: the finish kernel adds them one by one
+  if (lane < EP) db_s[w][lane] = db;
+  if (lane == 0) loss_s[w] = loss_w;
+  __syncthreads();
+  if (threadIdx.x < EP && a.grads) {
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) sum += db_s[k][threadIdx.x];
+    a.db_part[(size_t)blockIdx.x * EP + threadIdx.x] = sum;
+  }
+  if (threadIdx.x == 0) {
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) sum += loss_s[k];
+    a.blk_loss[blockIdx.x] = sum;
   }
 }
 
@@ -1206,7 +1239,7 @@ __global__ void __launch_bounds__(128) seq_grads_f32_kernel(SeqBalArgs a) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const bool in = tb + u < t_end;
-        xv[u] = in ? __ldg(reinterpret_cast<const float4*>(x + (size_t)(tb + u) * D)) : zero;
+        xv[u] = in ? ld_past_l1(x + (size_t)(tb + u) * D) : zero;
         o[u] = in && dx && a.accumulate ? *reinterpret_cast<const float4*>(dx + (size_t)(tb + u) * D) : zero;
       }
 #pragma unroll
@@ -1266,7 +1299,7 @@ __device__ __forceinline__ double block_sum_f64(double v, double* sh) {
 
 // Blocks by role, all sums in a fixed order: 32 elements of dWg each (8 warps over the ranges); one for
 // each expert's db; one for each sequence's loss; one for the mean loss.
-// db sums `db_rows` rows of ep values: dl's own rows (fp32) or the scores kernel's sums of 16.
+// db sums `db_rows` rows of ep values: dl's own rows (fp32, few tokens) or the kernels' sums over tokens.
 __global__ void __launch_bounds__(kFinThreads) seq_finish_kernel(SeqBalArgs a, const float* db_in, int db_rows, int ep,
                                                                  int wg_blocks, int db_blocks) {
   __shared__ double sh[kFinThreads / 32];
@@ -1379,7 +1412,7 @@ cudaError_t launch16(const SeqBalArgs& a, cudaStream_t s) {
 template <int EP>
 cudaError_t launch32(const SeqBalArgs& a, cudaStream_t s) {
   cudaError_t e = a.T <= kSbF32Single ? chained<seq_scores_f32_kernel<EP, 1>, 0>((a.T + 3) / 4, 128, 0, s, a)
-                                      : chained<seq_scores_f32_kernel<EP, 4>, 0>((a.T + 15) / 16, 128, 0, s, a);
+                                      : chained<seq_scores_f32_kernel<EP, EP == 8 ? 4 : 2>, 0>((a.T + 15) / 16, EP == 8 ? 128 : 256, 0, s, a);
   if (e != cudaSuccess || !a.grads) return e;
   return chained<seq_grads_f32_kernel<EP>, EP * 2048>((a.D + 127) / 128 * a.groups, 128, EP * 2048, s, a);
 }
@@ -1401,7 +1434,7 @@ size_t seq_balance_frag_bytes(int E, int dtype) {
 }
 
 bool seq_balance_fused(int D, int E, int dtype) {
-  if (dtype == MOE_F32 || E > 16 || D / 32 > kFuCols * kFuGroups) return false;
+  if (dtype == MOE_F32 || E > 16 || D < kFuMinD || D / 32 > kFuCols * kFuGroups) return false;
   return fused_plan(D, E <= 8 ? 1 : 2, (int)(seq_balance_frag_bytes(E, dtype) / 512), true).stages >= 2;
 }
 
@@ -1441,10 +1474,10 @@ cudaError_t launch_seq_balance(const SeqBalArgs& a, cudaStream_t s) {
     e = a.dtype == MOE_F16 ? launch16_e<true>(a, s) : launch16_e<false>(a, s);
   if (e != cudaSuccess) return e;
   const int wg_blocks = a.dwg ? a.E * a.D / 32 : 0, db_blocks = a.dbias ? a.E : 0;
-  const bool f32 = a.dtype == MOE_F32;
-  const int db_rows = f32 ? a.T : a.fused ? a.groups * kFuRouters : (a.T + 15) / 16;
+  const bool one = a.dtype == MOE_F32 && a.T <= kSbF32Single;   // db and the losses token by token
+  const int db_rows = one ? a.T : a.fused ? a.groups * kFuRouters : (a.T + 15) / 16;
   return chained<seq_finish_kernel, 0>(wg_blocks + db_blocks + a.n_seqs + 1, kFinThreads, 0, s, a,
-                 (const float*)(f32 ? a.dl : a.db_part), db_rows, seq_balance_ep(a.E), wg_blocks, db_blocks);
+                 (const float*)(one ? a.dl : a.db_part), db_rows, seq_balance_ep(a.E), wg_blocks, db_blocks);
 }
 
 }  // namespace moe
