@@ -1282,7 +1282,7 @@ int moe_grad_norm(const moe_adamw_tensor_t* tensors, int32_t n_tensors, double g
   const size_t need = moe_grad_norm_workspace_size(n_tensors);
   if (ws_bytes < need) return fail(MOE_ERR_WORKSPACE, "ws_bytes=%zu < %zu", ws_bytes, need);
   const cudaError_t e = launch_grad_norm(tensors, n_tensors, grad_mult, max_norm, static_cast<OptCtl*>(ctl),
-                                         static_cast<double*>(ws), num_sms_current(), (cudaStream_t)stream);
+                                         static_cast<double*>(ws), (cudaStream_t)stream);
   return e == cudaSuccess ? ok() : cuda_fail(e, "gradient norm");
 }
 

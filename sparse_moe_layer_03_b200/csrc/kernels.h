@@ -325,7 +325,7 @@ struct OptCtl {
 size_t grad_norm_scratch(int n);
 cudaError_t launch_optim_init(OptCtl* c, long long step, double b1t, double b2t, cudaStream_t s);
 cudaError_t launch_grad_norm(const moe_adamw_tensor_t* t, int n, double mult, double max_norm, OptCtl* ctl, double* parts,
-                             int sms, cudaStream_t s);
+                             cudaStream_t s);
 cudaError_t launch_adamw(const moe_adamw_t& h, const moe_adamw_tensor_t* t, int n, OptCtl* ctl, int sms, cudaStream_t s);
 
 }  // namespace moe

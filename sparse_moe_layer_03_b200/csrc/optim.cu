@@ -20,10 +20,17 @@
 // bits for each moment are a hash of (seed, step, tensor, element): a call has no
 // other state, and repeats bit for bit.
 //
-// One block is 256 threads on a chunk of 2048 elements; a warp owns 256 of them,
-// eight consecutive ones in each lane, so that a warp's elements are exactly one
-// scale's and every fp32 stream moves in 32-byte vectors (two of 16 bytes where a
-// tensor is aligned to no more).
+// A block is 256 threads on chunks of 2048 elements; a warp owns 256 elements of a
+// chunk, eight consecutive ones in each lane, so that they are exactly one scale's and
+// every fp32 stream moves in 32-byte vectors (two of 16 bytes where a tensor is aligned
+// to no more).  With fp32 moments there is a block for every chunk: handed out in order
+// they keep each stream's traffic within a narrow window of memory, which DRAM rewards
+// (a probe that only moves these streams: 6.86 TB/s, against 6.05 from one wave of
+// blocks that walk the chunks in strides and drift apart).  106 M parameters, clipped,
+// with moving average and 16-bit copy: 673 us (norm included), 740 with one wave.  With
+// 8-bit moments the arithmetic weighs as much, and what a block works out before its
+// first chunk counts: one wave, 334 us; a block for every chunk 361 to 380, for every
+// eight adjacent ones 389.
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -36,11 +43,13 @@ namespace {
 constexpr int kOptThreads = 256;
 constexpr int kOptChunk = kOptThreads * 8;         // elements of a block's chunk
 constexpr int kOptPerSm = 4;                       // resident blocks: 64 registers a thread
+constexpr int kOptCountInside = 1184;              // blocks up to which they count the step themselves: 50,000 additions to
+                                                   // one word cost 60 us, a kernel for it 2
 constexpr int kScaleBlock = 256;                   // elements that share a scale
 constexpr int kNormChunk = kOptThreads * 16;
 constexpr int kOptSmall = 40, kOptLarge = 340;     // tensors a launch's parameters hold: under 4 KB, under 32 KB
 constexpr int kNormSmall = 140, kNormLarge = 1100;
-constexpr int kNormMaxBlocks = 2048;
+constexpr int kNormMaxBlocks = 2048;               // on every device: the sum's order is part of the result
 
 // Tensor of a chunk: the first whose chunks end behind it.
 __device__ __forceinline__ int find_tensor(const int* chunk_end, int n, int chunk) {
@@ -187,11 +196,24 @@ struct AdamwParams {
   OptTensor t[CAP];
   int chunk_end[CAP];
   int tensors, chunks;
-  int clipped, last;
+  int clipped, last;       // last: 1 or 2 for the call's last launch; 2: its blocks count the step
   double lr, beta1, beta2, eps, ema_decay, mult;
   unsigned long long seed;
   OptCtl* ctl;
 };
+
+__device__ __forceinline__ void count_step(OptCtl& c, bool skip, double beta1, double beta2) {
+  if (skip) {
+    c.skipped += 1;
+  } else {
+    c.step += 1;
+    c.beta1_t *= beta1;
+    c.beta2_t *= beta2;
+  }
+}
+__global__ void adamw_count_kernel(OptCtl* c, int clipped, double beta1, double beta2) {
+  count_step(*c, clipped && c->nonfinite, beta1, beta2);
+}
 
 // One step's scalars.
 struct StepScalars {
@@ -435,18 +457,11 @@ __global__ void __launch_bounds__(kOptThreads, kOptPerSm) adamw_kernel(const __g
     }
   }
   // the last block of the call's last launch counts the step: every block has read the control block
-  if (a.last && tid == 0) {
+  if (a.last == 2 && tid == 0) {
     __threadfence();
     if (atomicAdd(&a.ctl->step_done, 1u) == gridDim.x - 1) {
-      OptCtl& c = *a.ctl;
-      if (s.skip) {
-        c.skipped += 1;
-      } else {
-        c.step = s.t;
-        c.beta1_t *= a.beta1;
-        c.beta2_t *= a.beta2;
-      }
-      c.step_done = 0;
+      count_step(*a.ctl, s.skip, a.beta1, a.beta2);
+      a.ctl->step_done = 0;
     }
   }
 }
@@ -463,7 +478,7 @@ __global__ void optim_init_kernel(OptCtl* c, long long step, double b1t, double 
 
 template <int CAP>
 cudaError_t norm_launch(const moe_adamw_tensor_t* t, int n, double mult, double max_norm, OptCtl* ctl, double* parts,
-                        int* part0, bool last, int blocks_max, cudaStream_t s) {
+                        int* part0, bool last, cudaStream_t s) {
   static_assert(sizeof(NormParams<CAP>) <= 32764, "kernel parameters");
   NormParams<CAP> a;
   long long chunks = 0;
@@ -481,7 +496,7 @@ cudaError_t norm_launch(const moe_adamw_tensor_t* t, int n, double mult, double 
   a.part0 = *part0;
   a.last = last;
   a.mult = mult; a.max_norm = max_norm; a.ctl = ctl; a.parts = parts;
-  const int grid = (int)(chunks < 1 ? 1 : chunks < blocks_max ? chunks : blocks_max);
+  const int grid = (int)(chunks < 1 ? 1 : chunks < kNormMaxBlocks ? chunks : kNormMaxBlocks);
   *part0 += grid;
   a.nparts = *part0;
   grad_norm_kernel<CAP><<<grid, kOptThreads, 0, s>>>(a);
@@ -511,12 +526,13 @@ cudaError_t adamw_launch(const moe_adamw_t& h, const moe_adamw_tensor_t* t, int 
     a.chunk_end[a.tensors++] = (int)chunks;
   }
   a.chunks = (int)chunks;
-  a.clipped = h.clipped; a.last = last;
+  a.clipped = h.clipped;
   a.lr = h.lr; a.beta1 = h.beta1; a.beta2 = h.beta2; a.eps = h.eps; a.ema_decay = h.ema_decay; a.mult = h.grad_mult;
   a.seed = h.seed;
   a.ctl = ctl;
-  const long long most = (long long)sms * kOptPerSm;   // one wave
-  const int grid = (int)(chunks < 1 ? 1 : chunks < most ? chunks : most);
+  const long long wave = (long long)sms * kOptPerSm;
+  const int grid = (int)(chunks < 1 ? 1 : Q8 && chunks > wave ? wave : chunks);
+  a.last = !last ? 0 : grid <= kOptCountInside ? 2 : 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kOptThreads);
@@ -526,7 +542,10 @@ cudaError_t adamw_launch(const moe_adamw_t& h, const moe_adamw_tensor_t* t, int 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, adamw_kernel<Q8, CAP>, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, adamw_kernel<Q8, CAP>, a);
+  if (e != cudaSuccess || a.last != 1) return e;
+  adamw_count_kernel<<<1, 1, 0, s>>>(ctl, h.clipped, h.beta1, h.beta2);
+  return cudaGetLastError();
 }
 
 template <bool Q8>
@@ -553,14 +572,13 @@ cudaError_t launch_optim_init(OptCtl* c, long long step, double b1t, double b2t,
 }
 
 cudaError_t launch_grad_norm(const moe_adamw_tensor_t* t, int n, double mult, double max_norm, OptCtl* ctl, double* parts,
-                             int sms, cudaStream_t s) {
+                             cudaStream_t s) {
   int part0 = 0;
-  const int most = sms * 8 < kNormMaxBlocks ? sms * 8 : kNormMaxBlocks;
-  if (n <= kNormSmall) return norm_launch<kNormSmall>(t, n, mult, max_norm, ctl, parts, &part0, true, most, s);
+  if (n <= kNormSmall) return norm_launch<kNormSmall>(t, n, mult, max_norm, ctl, parts, &part0, true, s);
   for (int first = 0; first < n; first += kNormLarge) {
     const int k = n - first < kNormLarge ? n - first : kNormLarge;
     const cudaError_t e =
-        norm_launch<kNormLarge>(t + first, k, mult, max_norm, ctl, parts, &part0, first + k == n, most, s);
+        norm_launch<kNormLarge>(t + first, k, mult, max_norm, ctl, parts, &part0, first + k == n, s);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
