@@ -490,7 +490,8 @@ int moe_expert_frequency(const moe_config_t* cfg, const int32_t* topk_idx, const
  *   seq_counts  [n_seqs,E] int32 out: selected pairs of each sequence and expert
  *   seq_loss    [n_seqs] fp32 out; loss [1] fp32 out
  *   dwg         [E,D] fp32 out, or NULL for the loss and the counts alone (then dbias and dx too)
- *   dbias       [E] fp32 out or NULL; dx [T,D] act out or NULL; dx_accumulate 1: dx += the router's part
+ *   dbias       [E] fp32 out or NULL; dx [T,D] act out or NULL, not x; dx_accumulate 1: dx += the
+ *               router's part
  *   bws         scratch of moe_seq_balance_workspace_size(cfg, n_seqs) bytes, 256-byte aligned
  *   ws          status word only: offsets that descend or leave 0..T, or an expert id >= E (which is
  *               skipped), are reported through moe_check_status
@@ -570,7 +571,8 @@ int moe_grad_norm(const moe_adamw_tensor_t* tensors, int32_t n_tensors, double g
 /*
  * moe_adamw_step -- one step of every tensor (see above), which ctl then counts.  The list and the
  * settings are host memory, read before the call returns.  Tensors must not overlap.  One launch
- * for up to 340 tensors; no scratch.  A captured call replays as the next step.
+ * for up to 340 tensors, and a small one that counts the step where they are large; no scratch.
+ * A captured call replays as the next step.
  */
 int moe_adamw_step(const moe_adamw_t* settings, const moe_adamw_tensor_t* tensors, int32_t n_tensors, void* ctl,
                    void* stream);

@@ -399,6 +399,21 @@ def test_python_refusals():
     assert opt.steps_taken() == 0
 
 
+@pytest.mark.parametrize("n", [1184 * 2048, 1184 * 2048 + 1, 5_000_000])
+def test_steps_are_counted_once_whatever_the_blocks(n):
+    # up to 1184 blocks count the step themselves, more leave it to a kernel of its own
+    p = torch.zeros(n, device=DEV)
+    g = torch.ones(n, device=DEV)
+    opt = optim.AdamW([p], lr=1.0, betas=(0.5, 0.5), eps=0.0)
+    for t in range(1, 4):
+        opt.step([g])                                     # m / c1 = sqrt(v / c2) = 1: every step moves by 1
+        assert opt.steps_taken() == t
+        assert float((p + t).abs().max()) <= t * 16 * U
+    g[n - 1] = float("inf")
+    opt.step([g], max_norm=1.0)
+    assert opt.steps_taken() == 3 and int(opt.skipped) == 1 and float((p + 3).abs().max()) <= 48 * U
+
+
 def test_offsets_beyond_32_bits():
     # 2^31 + 300 elements: byte offsets pass 2^33 in the master, element offsets 2^31
     n = 2 ** 31 + 300
