@@ -227,9 +227,11 @@ def test_full_size_with_many_sequences(dt):
     c.check(c.run())
 
 
-@pytest.mark.parametrize("dt", list(TYPES))
-def test_equal_bits_again_captured_and_on_another_stream(dt):
-    c = Case(1000, 384, 8, 2, dt, offsets=[0, 400, 990])
+@pytest.mark.parametrize("dt,T,D,E", [("f32", 1000, 384, 8), ("bf16", 1000, 384, 8), ("f16", 1000, 384, 8),
+                                      ("bf16", 3000, 768, 8), ("f16", 5000, 512, 16), ("f32", 6000, 128, 20),
+                                      ("bf16", 3000, 320, 24)])
+def test_equal_bits_again_captured_and_on_another_stream(dt, T, D, E):
+    c = Case(T, D, E, 2, dt, offsets=[0, 400, T - 10])
     want = c.run(accumulate=False)
     want = {k: v.clone() for k, v in want.items()}
     side = torch.cuda.Stream()
@@ -253,8 +255,9 @@ def test_equal_bits_again_captured_and_on_another_stream(dt):
         assert torch.equal(want[k], o[k]), k
 
 
-def test_two_calls_at_once_on_two_streams():
-    cases = [Case(900, 256, 8, 2, "bf16", offsets=[0, 900], seed=s) for s in (1, 2)]
+@pytest.mark.parametrize("T,D", [(900, 256), (4000, 768)])
+def test_two_calls_at_once_on_two_streams(T, D):
+    cases = [Case(T, D, 8, 2, "bf16", offsets=[0, T], seed=s) for s in (1, 2)]
     want = [c.run() for c in cases]
     want = [{k: v.clone() for k, v in w.items()} for w in want]
     streams = [torch.cuda.Stream() for _ in cases]
