@@ -50,9 +50,8 @@ class _Control:
         self.grad_scale = self.ctl[32:36].view(torch.float32)
         self.nonfinite = self.ctl[36:40].view(torch.int32)
         self.skipped = self.ctl[40:48].view(torch.int64)         # steps that a non-finite gradient left out
-        self._ws = None
-
         self._ctl_ptr, self._ws_for = self.ctl.data_ptr(), -1
+        self._ws = []                                            # the last is the one in use; a captured graph may hold another
 
     def _init(self, step, betas):
         with torch.cuda.device(self.device):
@@ -60,8 +59,11 @@ class _Control:
 
     def _norm(self, tensors, n, max_norm, grad_mult, stream):
         if self._ws_for < n:
-            self._ws = torch.empty(B.moe_grad_norm_workspace_size(n), dtype=torch.uint8, device=self.device)
-            self._ws_ptr, self._ws_bytes, self._ws_for = self._ws.data_ptr(), self._ws.numel(), n
+            need = B.moe_grad_norm_workspace_size(n)
+            if not self._ws or self._ws_bytes < need:
+                self._ws.append(torch.empty(need, dtype=torch.uint8, device=self.device))
+                self._ws_ptr, self._ws_bytes = self._ws[-1].data_ptr(), need
+            self._ws_for = n
         B.moe_grad_norm(tensors, n, grad_mult, max_norm, self._ctl_ptr, self._ws_ptr, self._ws_bytes, stream)
 
     def _on_device(self, call, *args):
@@ -197,6 +199,7 @@ class AdamW(_Control):
 
     def steps_taken(self) -> int:
         """Steps taken so far (waits for the device)."""
+        torch.cuda.synchronize(self.device)
         return int(self._step.item())
 
     def part(self, name: str, i: int) -> torch.Tensor:
@@ -225,14 +228,18 @@ class AdamW(_Control):
 
     def state_dict(self) -> dict:
         """Copies of the state and the step count (waits for the device)."""
-        return dict({k: b.clone() for k, b in self.buffers.items()}, step=self.steps_taken())
+        step = self.steps_taken()
+        return dict({k: b.clone() for k, b in self.buffers.items()}, step=step)
 
     def load_state_dict(self, state: dict):
+        """Take up a ``state_dict``.  ``lr_scale`` is 1 and ``skipped`` 0 again."""
         if set(state) != set(self.buffers) | {"step"}:
             raise ValueError(f"state has {sorted(state)}, not {sorted(self.buffers) + ['step']}")
         for k, b in self.buffers.items():
             if state[k].shape != b.shape or state[k].dtype != b.dtype:
                 raise ValueError(f"state[{k!r}] is {tuple(state[k].shape)} {state[k].dtype}, not {tuple(b.shape)} {b.dtype}")
+        if int(state["step"]) < 0:
+            raise ValueError(f"state['step'] is {state['step']}")
         for k, b in self.buffers.items():
             b.copy_(state[k])
         self._init(int(state["step"]), self.betas)
@@ -261,3 +268,19 @@ class LayerAdamW(AdamW):
 
     def step(self, grads: dict, max_norm: Optional[float] = None, grad_mult: float = 1.0):
         super().step([grads[n] for n in self.grad_names], max_norm, grad_mult)
+
+    def state_dict(self) -> dict:
+        """Copies of the state, the step count and the masters (waits for the device)."""
+        return dict(super().state_dict(), params=[p.clone() for p in self.params])
+
+    def load_state_dict(self, state: dict):
+        """Take up a ``state_dict``: the layer's weights become those of its masters."""
+        state = dict(state)
+        params = state.pop("params", ())
+        if [p.shape for p in params] != [p.shape for p in self.params]:
+            raise ValueError("state['params'] does not fit the layer's weights")
+        super().load_state_dict(state)
+        for p, w, saved in zip(self.params, self.weights, params):
+            p.copy_(saved)
+            if w is not None:
+                w.copy_(p)

@@ -450,3 +450,66 @@ def test_a_layer_is_trained_by_its_own_step():
     assert opt.params[5].data_ptr() == L.router_bias.data_ptr()      # fp32: its own master
     L.forward(x)                                                    # and the next forward runs on them
     L.check()
+
+
+def test_a_captured_norm_keeps_its_scratch():
+    # more tensors than one launch takes need more scratch; the graph's own must outlive that
+    norm = optim.GradNorm(DEV)
+    g = [torch.full((100,), 2.0, device=DEV)]
+    norm(g)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        norm(g)
+    held = list(norm._ws)
+    many = [torch.ones(1, device=DEV) for _ in range(1200)]
+    assert abs(float(norm(many)[0]) - 1200 ** 0.5) <= 1200 ** 0.5 * U
+    assert len(norm._ws) == 2 and norm._ws[0] is held[0]
+    graph.replay()
+    torch.cuda.synchronize()
+    assert float(norm.grad_norm) == 20.0
+
+
+def test_the_step_count_waits_for_other_streams():
+    p = torch.ones(1000, device=DEV)
+    opt = optim.AdamW([p], lr=1e-3)
+    g = torch.ones(1000, device=DEV)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)                     # some 10 ms
+        opt.step([g])
+    assert opt.steps_taken() == 1
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+        opt.step([g])
+    assert opt.state_dict()["step"] == 2
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_a_layers_optimizer_resumes_with_its_masters(dt):
+    from sparse_moe_layer_03_b200.layer import LayerShape, MoELayer
+    w = I.small_workload(64, 64, 128, 4, 2, 1, dt, "topk", seed=3)
+    inp = I.make_inputs(w)
+    make = lambda: MoELayer(LayerShape(w.T, w.D, w.H, w.E, w.K, w.n_shared, w.dtype, w.routing, w.alpha), inp)  # noqa: E731
+    layer, gen = make(), torch.Generator().manual_seed(9)
+    settings = dict(lr=1e-4, weight_decay=0.1, state="e4m3", ema_decay=0.9, seed=2)
+    opt = layer.optimizer(**settings)
+    grads = [{n: _rand(p.numel(), gen) for n, p in zip(opt.grad_names, opt.params)} for _ in range(2)]
+    opt.step(grads[0])
+    saved = opt.state_dict()
+    opt.step(grads[1])
+    again = make()
+    other = again.optimizer(**settings)
+    other.load_state_dict(saved)
+    for p, wt in zip(other.params, other.weights):
+        assert wt is None or torch.equal(p.to(wt.dtype), wt)
+    other.step(grads[1])
+    for a, b in zip(opt.params + [t for t in opt.weights if t is not None],
+                    other.params + [t for t in other.weights if t is not None]):
+        assert torch.equal(a, b)
+    assert torch.equal(layer.w1, again.w1) and other.steps_taken() == 2
+    for bad in (dict(saved, params=saved["params"][:-1]), {k: v for k, v in saved.items() if k != "params"},
+                dict(saved, step=-1)):
+        with pytest.raises(ValueError):
+            other.load_state_dict(bad)
