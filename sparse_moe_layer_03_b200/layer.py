@@ -249,6 +249,14 @@ class MoELayer:
         ``seq_len`` tokens.  ``grads`` (a dict with dwg, dbias, dx) receives the router's gradients of
         aux_scale * balance_loss, with those of the gates ``dgate``; its dx is added to."""
         s, dev = self.s, self.device
+        g = grads or {}
+        f32, T = torch.float32, self.cfg.T
+        for name, t, dt, shape in (("x", x, self.act_dtype, (T, s.D)), ("dgate", dgate, f32, (T, self.kmax)),
+                                   ("dwg", g.get("dwg"), f32, (s.E, s.D)), ("dbias", g.get("dbias"), f32, (s.E,)),
+                                   ("dx", g.get("dx"), self.act_dtype, (T, s.D))):
+            if (t is not None or name == "x") and (t.shape != shape or t.dtype != dt or t.device != self.wg.device
+                                                   or not t.is_contiguous()):
+                raise ValueError(f"{name} must be a contiguous {dt} tensor {list(shape)} on the layer's device")
         if seq_offsets is None:
             n = self.cfg.T // s.seq_len if s.seq_len else min(self.cfg.T, 1)
         else:
@@ -262,11 +270,10 @@ class MoELayer:
         out = {"seq_counts": torch.empty((n, s.E), dtype=torch.int32, device=dev),
                "seq_loss": torch.empty((n,), dtype=torch.float32, device=dev),
                "balance_loss": torch.empty((1,), dtype=torch.float32, device=dev)}
-        g = grads or {}
         B.moe_seq_balance(self.cfg, x, self.wg, self.router_bias, seq_offsets, n, self.topk_idx, self.n_sel, dgate,
                           aux_scale, out["seq_counts"], out["seq_loss"], out["balance_loss"], g.get("dwg"),
-                          g.get("dbias"), g.get("dx"), int("dx" in g), self._sbws, self._sbws.numel(), self.ws,
-                          self.stream())
+                          g.get("dbias"), g.get("dx"), int(g.get("dx") is not None), self._sbws, self._sbws.numel(),
+                          self.ws, self.stream())
         return out
 
     def backward(self, x: torch.Tensor, dout: torch.Tensor, aux_scale: float = 1.0,

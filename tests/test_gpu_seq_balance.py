@@ -386,3 +386,26 @@ def test_a_layer_trained_on_the_loss_per_image(how, routing):
     out = layer.forward(x)                                       # and on the new weights
     layer.check()
     assert torch.isfinite(out).all()
+
+
+def test_a_layer_refuses_tensors_that_do_not_fit():
+    w = I.small_workload(64, 64, 128, 4, 2, 0, "bf16", "topk", seed=3)
+    inp = I.make_inputs(w)
+    from sparse_moe_layer_03_b200.layer import LayerShape, MoELayer
+    layer = MoELayer(LayerShape(w.T, w.D, w.H, w.E, w.K, w.n_shared, w.dtype, w.routing, w.alpha), inp)
+    x = torch.as_tensor(inp["x"]).to(DEV, layer.act_dtype)
+    layer.forward(x)
+    g = dict(dwg=torch.zeros(4, 64, device=DEV))
+    off = torch.tensor([0, 64], dtype=torch.int32, device=DEV)
+    bad = [dict(x=x[:63]), dict(x=x.float()), dict(x=x.cpu()), dict(x=x.t().contiguous().t()),
+           dict(dgate=torch.zeros(64, 3, device=DEV), grads=g), dict(dgate=torch.zeros(64, 2, device=DEV).half(), grads=g),
+           dict(grads=dict(dwg=torch.zeros(4, 63, device=DEV))), dict(grads=dict(g, dbias=torch.zeros(5, device=DEV))),
+           dict(grads=dict(g, dx=torch.zeros(64, 64, device=DEV))), dict(seq_offsets=off.long()), dict(seq_offsets=off.cpu()),
+           dict(seq_offsets=off[:0])]
+    for kw in bad:
+        with pytest.raises(ValueError):
+            layer.seq_balance(kw.pop("x", x), **kw)
+    out = layer.seq_balance(x, off, grads=dict(g, dbias=None, dx=None))
+    torch.cuda.synchronize()
+    layer.check()
+    assert int(out["seq_counts"].sum()) == 64 * 2
