@@ -568,6 +568,13 @@ def e4m3_round(a, r16):
     return np.minimum(np.floor(q) * gap, 448.0), np.abs(q - np.rint(q))
 
 
+def e4m3_round_root(a, r16):
+    """`e4m3_round` of the second moment's root: the smallest code, 2^-9, at least where it is not zero (an
+    element whose first moment is kept must not lose what that is divided by)."""
+    val, room = e4m3_round(a, r16)
+    return np.where(as_f64(a) > 0, np.maximum(val, 2.0 ** -9), val), room
+
+
 # ---------------------------------------------------------------- balance loss over packed sequences
 
 def balance_packed(idx, P, K, alpha, offsets):

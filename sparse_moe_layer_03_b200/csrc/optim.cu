@@ -18,7 +18,11 @@
 // v where it is for ever; codes are rounded up or down at random instead, up with
 // the probability that makes the stored value right on average.  The 16 random
 // bits for each moment are a hash of (seed, step, tensor, element): a call has no
-// other state, and repeats bit for bit.
+// other state, and repeats bit for bit.  A root that is not zero keeps a code of 1
+// (4.4e-6 of its block's largest) at least: were it rounded to zero while the same
+// element's first moment is not, the next step would divide that by little more than eps
+// (one gradient of 1 among others of 1e-6: moves of 500 lr, against 1.6 with the floor).
+// The average of such roots is too large, and their elements' steps the shorter.
 //
 // A block is 256 threads on chunks of 2048 elements; a warp owns 256 elements of a
 // chunk, eight consecutive ones in each lane, so that they are exactly one scale's and
@@ -406,7 +410,7 @@ __global__ void __launch_bounds__(kOptThreads, kOptPerSm) adamw_kernel(const __g
         for (int q = 0; q < 8; ++q) {
           const uint32_t rnd = element_bits(klo + q, key_hi);
           zm[q] = e4m3_random(__fmul_rn(m[q], mi), __byte_perm(rnd, 0u, 0x4104)) | (__float_as_uint(m[q]) & 0x80000000u);
-          zv[q] = e4m3_random(__fmul_rn(r[q], vi), __byte_perm(rnd, 0u, 0x4324));
+          zv[q] = max(e4m3_random(__fmul_rn(r[q], vi), __byte_perm(rnd, 0u, 0x4324)), r[q] > 0.f ? 0x01000000u : 0u);
         }
         mc = make_uint2(top_bytes(zm[0], zm[1], zm[2], zm[3]), top_bytes(zm[4], zm[5], zm[6], zm[7]));
         vc = make_uint2(top_bytes(zv[0], zv[1], zv[2], zv[3]), top_bytes(zv[4], zv[5], zv[6], zv[7]));
