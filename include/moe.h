@@ -517,8 +517,9 @@ int moe_seq_balance(const moe_config_t* cfg, const void* x, const void* wg, cons
  * step, place of the tensor in the list, element): equal calls give equal bits.  A root above zero
  * keeps the smallest code (4.4e-6 of its block's largest) at least, so that no first moment outlives
  * what it is divided by; on average an element that far below its largest moves by less than lr.
- * A block of 256 whose largest moment is below 2^-100 or not finite is stored as zeros.  The
- * denominator is at least 2^-126 (eps = 0 with no gradient at all leaves a parameter as it is).
+ * A block of 256 whose largest moment is below 2^-100 or not finite is stored as zeros; first
+ * moments also where the second are not finite.  The denominator is at least 2^-126 (eps = 0 with
+ * no gradient at all leaves a parameter as it is).
  */
 typedef enum { MOE_MOMENTS_F32 = 0, MOE_MOMENTS_E4M3 = 1 } moe_moments_t;
 

@@ -393,8 +393,10 @@ __global__ void __launch_bounds__(kOptThreads, kOptPerSm) adamw_kernel(const __g
         // non-negative floats order as their bits do, and a NaN lies above them
         mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
         vx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vx)));
-        // a block whose largest moment is below 2^-100, or not finite, becomes zero
-        const bool mok = mx >= 7.888609052210118e-31f && mx < INFINITY, vok = vx >= 7.888609052210118e-31f && vx < INFINITY;
+        // a block whose largest moment is below 2^-100, or not finite, becomes zero; first moments also where the
+        // second are not finite (gradients from 1.8e19 on): they would be divided by the next gradient alone
+        const bool mok = mx >= 7.888609052210118e-31f && mx < INFINITY && vx < INFINITY;
+        const bool vok = vx >= 7.888609052210118e-31f && vx < INFINITY;
         const float mi = mok ? __fmul_rn(__frcp_rn(mx), 448.f) : 0.f, vi = vok ? __fmul_rn(__frcp_rn(vx), 448.f) : 0.f;
         const uint32_t klo = key_lo + (uint32_t)i0;
         if (!mok) {

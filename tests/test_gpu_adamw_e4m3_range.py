@@ -1,4 +1,4 @@
-"""8-bit moments over blocks whose elements span many powers of two.
+"""8-bit moments over blocks whose elements span many powers of two, and past fp32's range.
 
 Constant gradients, one element of each block S and the others far smaller.  The block's scales are S's,
 whose stored moments are exact, so that AdamW moves every element by lr (1 at most, eps lowers it).  Let a
@@ -49,3 +49,26 @@ def test_a_root_of_zero_stays_zero():
     codes = opt.buffers["v"].view(torch.uint8)
     assert torch.equal(torch.nonzero(codes).flatten().cpu(), torch.tensor([0, 299]))
     assert int(torch.count_nonzero(p)) == 2
+
+
+def test_a_second_moment_past_fp32_takes_the_first_with_it():
+    # 1e25 squared is infinite in fp32: its block's second moments start again from zero, and a first moment
+    # that stayed would then be divided by the next step's gradient alone
+    lr = 1e-3
+    gen = torch.Generator().manual_seed(3)
+    p = torch.zeros(1024, device=DEV)
+    opt = optim.AdamW([p], lr=lr, state="e4m3", seed=1)
+    g = (torch.rand(1024, generator=gen) + 0.5).to(DEV)
+    opt.step([g])
+    big = g.clone()
+    big[300] = 1e25
+    opt.step([big])
+    assert torch.isfinite(p).all()
+    assert float(opt.part("v_scale", 0)[1]) == 0.0 and float(opt.part("m_scale", 0)[1]) == 0.0
+    for _ in range(4):
+        had = p.clone()
+        opt.step([g])
+        # a first step's own ratio at step t: (1 - b1) g / c1 over sqrt(1 - b2) g / sqrt(c2), largest 0.1 / 0.2
+        # over sqrt(0.001 / 0.003) = 0.9 at t = 3, rising to 3.2 as t grows; below 4 with the codes' eighths
+        assert float((p - had).abs().max()) <= 4 * lr
+    assert torch.isfinite(opt.buffers["m_scale"]).all() and torch.isfinite(opt.buffers["v_scale"]).all()
