@@ -495,7 +495,9 @@ int moe_expert_frequency(const moe_config_t* cfg, const int32_t* topk_idx, const
  *   bws         scratch of moe_seq_balance_workspace_size(cfg, n_seqs) bytes, 256-byte aligned
  *   ws          status word only: offsets that descend or leave 0..T, or an expert id >= E (which is
  *               skipped), are reported through moe_check_status
- * Every type; fixed-order sums, bit-reproducible.
+ * Every type; fixed-order sums, bit-reproducible.  The logits' gradient enters dwg as 24 bits (bf16), or as
+ * 22 bits below the expert's own largest of 16 consecutive tokens (fp16), and dx as 16 bits, or 22 below
+ * its token's largest; sums are fp32.
  */
 size_t moe_seq_balance_workspace_size(const moe_config_t* cfg, int32_t n_seqs);
 int moe_seq_balance(const moe_config_t* cfg, const void* x, const void* wg, const float* router_bias,

@@ -1135,7 +1135,7 @@ static SbLayout sb_layout(const moe_config_t* c) {
   L.tok_loss = take(T * 4);
   L.blk_loss = take(nblk * 4);
   L.frag = take(is16(c) ? nblk * seq_balance_frag_bytes(c->E, c->dtype) : 0);
-  L.scales = take(c->dtype == MOE_F16 ? nblk * 128 : 0);
+  L.scales = take(nblk * seq_balance_scale_bytes(c->E, c->dtype));
   L.dl = take(is16(c) ? 0 : T * ep * 4);
   // rows of the two kernels' token blocks, or four router warps of each block of the fused one
   L.db_part = take((nblk > 4 * (size_t)groups ? nblk : 4 * (size_t)groups) * ep * 4);

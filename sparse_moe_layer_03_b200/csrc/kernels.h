@@ -297,7 +297,7 @@ struct SeqBalArgs {
   float* tok_loss;                                    // [T]
   float* blk_loss;                                    // [blocks] sums of 16 of them, or null (fp32, few tokens)
   uint4* frag;                                        // 16-bit: dl in fragment order, seq_balance_frag_bytes a block
-  float4* scales;                                     // fp16: [blocks, 8] inverse scales of rows g, g + 8 and the block
+  float4* scales;                                     // fp16: inverse scales, seq_balance_scale_bytes a block
   float* dl;                                          // fp32: [T, ep]
   float* db_part;                                     // [blocks, ep] sums of dl over blocks of tokens
   float* partials;                                    // [groups, E, D]
@@ -307,6 +307,7 @@ constexpr int kSbSms = 148;                           // the plan (and so the su
 constexpr int kSbF32Single = 148 * 32;                // fp32: tokens up to which a warp takes one at a time
 int seq_balance_ep(int E);                            // experts rounded up to 8, 16 or 32
 size_t seq_balance_frag_bytes(int E, int dtype);
+size_t seq_balance_scale_bytes(int E, int dtype);
 bool seq_balance_fused(int D, int E, int dtype);      // else the shape takes the two kernels
 void seq_balance_plan(int T, int D, int E, int dtype, int* groups, int* blocks_per_range);
 cudaError_t launch_seq_balance(const SeqBalArgs& a, cudaStream_t s);

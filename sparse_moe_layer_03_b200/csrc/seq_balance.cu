@@ -27,7 +27,8 @@
 // tokens, whose pairs lie in different rows: two rows' pieces are interleaved in registers.
 // dl goes between the kernels already in fragment order, as it is and transposed (movmatrix), in
 // 16-bit parts that add up to it: for dx two; for dWg, which stays in fp32, three of bf16 (24 bits)
-// or two of fp16 (22 bits below the largest of its 16 tokens; each row of dx has a scale of its own).
+// or two of fp16 (22 bits below the largest of its expert's 16: a scale for each expert, so that the
+// gate row of one hardly ever chosen keeps its digits; for dx a scale for each token).
 // With E <= 8 two parts share one k16 step.
 #include <atomic>
 
@@ -217,6 +218,23 @@ template <int NE, bool F16> struct Parts {
   static constexpr int NK = NE <= 2 ? 1 : NE / 2;           // 16-expert tiles
   static constexpr int A = NE == 1 ? 1 : 2 * NK;            // for dx
   static constexpr int T = F16 ? A : NE == 1 ? 2 : 3 * NK;  // for dWg
+  static constexpr int V = !F16 ? 0 : NE == 4 ? 2 : 1;      // float4s of inverse scales for each row pair
+};
+// fp16's inverse scales of a 16-token block, as lane (g, c) takes them: of rows g and g + 8, and of experts
+// 8 nt + g.
+template <int NE> struct DlScales {
+  float row[2] = {1.f, 1.f}, expert[NE];
+  __device__ __forceinline__ void store(float4* p) const {
+    p[0] = make_float4(row[0], row[1], NE < 4 ? expert[0] : 0.f, NE == 2 ? expert[1 % NE] : 0.f);
+    if (NE == 4) p[1] = make_float4(expert[0], expert[1 % NE], expert[2 % NE], expert[3 % NE]);
+  }
+  __device__ __forceinline__ void load(const float4& u, const float4& v) {
+    row[0] = u.x;
+    row[1] = u.y;
+    const float e[4] = {NE == 4 ? v.x : u.z, NE == 4 ? v.y : u.w, v.z, v.w};
+#pragma unroll
+    for (int nt = 0; nt < NE; ++nt) expert[nt] = e[nt];
+  }
 };
 
 // The gates' gradients of a 16-token block, lane l < 16 holding token l's first slots: loaded ahead of
@@ -331,27 +349,35 @@ __device__ __forceinline__ void logits_to_dl(const SeqBalArgs& a, int rb, const 
 }
 
 // dl in fragment order: fa (k = experts) for dx, ft (k = tokens, by movmatrix) for dWg, and fp16's inverse
-// scales of rows g, g + 8 and the block.
+// scales.
 template <int NE, bool F16>
-__device__ __forceinline__ void dl_fragments(const RowPair<NE>& dl, uint4* fa, uint4* fw, float4& scale) {
+__device__ __forceinline__ void dl_fragments(const RowPair<NE>& dl, uint4* fa, uint4* fw, DlScales<NE>& scale) {
   using H = H16<F16>;
   using P = Parts<NE, F16>;
-  float sr[2] = {1.f, 1.f}, sb = 1.f;
+  float sr[2] = {1.f, 1.f}, se[NE][2];
   if (F16) {
-    float mr[2], inv[2], invb;
+    const int g = (threadIdx.x & 31) >> 2;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      mr[r] = 0.f;
+      float mr = 0.f;
 #pragma unroll
-      for (int nt = 0; nt < NE; ++nt) mr[r] = fmaxf(mr[r], fmaxf(fabsf(dl[r][nt][0]), fabsf(dl[r][nt][1])));
-      mr[r] = quad_max(mr[r]);
-      sr[r] = pow2_scale(mr[r], inv[r]);
+      for (int nt = 0; nt < NE; ++nt) mr = fmaxf(mr, fmaxf(fabsf(dl[r][nt][0]), fabsf(dl[r][nt][1])));
+      sr[r] = pow2_scale(quad_max(mr), scale.row[r]);
     }
-    float mb = fmaxf(mr[0], mr[1]);
 #pragma unroll
-    for (int o = 4; o < 32; o <<= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
-    sb = pow2_scale(mb, invb);
-    scale = make_float4(inv[0], inv[1], invb, 0.f);
+    for (int nt = 0; nt < NE; ++nt) {
+      float inv[2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        float me = fmaxf(fabsf(dl[0][nt][q]), fabsf(dl[1][nt][q]));
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) me = fmaxf(me, __shfl_xor_sync(0xffffffffu, me, o));
+        se[nt][q] = pow2_scale(me, inv[q]);
+      }
+      // expert 8 nt + g is a lane's with c = g / 2
+      const float even = __shfl_sync(0xffffffffu, inv[0], g >> 1), odd = __shfl_sync(0xffffffffu, inv[1], g >> 1);
+      scale.expert[nt] = g & 1 ? odd : even;
+    }
   }
   constexpr int NP = F16 ? 2 : 3;                  // parts
   uint32_t f[2][NP][NE], ft[2][NP][NE];
@@ -369,7 +395,7 @@ __device__ __forceinline__ void dl_fragments(const RowPair<NE>& dl, uint4* fa, u
         }
       };
       split(dl[r][nt][0] * sr[r], dl[r][nt][1] * sr[r], &f[r][0][nt], NE);
-      if (F16) split(dl[r][nt][0] * sb, dl[r][nt][1] * sb, &ft[r][0][nt], NE);
+      if (F16) split(dl[r][nt][0] * se[nt][0], dl[r][nt][1] * se[nt][1], &ft[r][0][nt], NE);
 #pragma unroll
       for (int i = 0; i < NP; ++i) ft[r][i][nt] = movm_t(F16 ? ft[r][i][nt] : f[r][i][nt]);
     }
@@ -475,9 +501,9 @@ __global__ void __launch_bounds__(kScWarps * 32) seq_scores_kernel(SeqBalArgs a)
     }
   using P = Parts<NE, F16>;
   uint4 fa[P::A], fw[P::T];
-  float4 scale;
+  DlScales<NE> scale;
   dl_fragments<NE, F16>(l, fa, fw, scale);
-  if (F16 && c == 0) a.scales[(size_t)rb * 8 + g] = scale;
+  if (F16 && c == 0) scale.store(a.scales + ((size_t)rb * 8 + g) * P::V);
   uint4* out = a.frag + (size_t)rb * (P::A + P::T) * 32 + lane;
 #pragma unroll
   for (int i = 0; i < P::A; ++i) out[i * 32] = fa[i];
@@ -494,7 +520,7 @@ __global__ void __launch_bounds__(kScWarps * 32) seq_scores_kernel(SeqBalArgs a)
 //        then holds columns 8c .. 8c+7 of rows g and g + 8, and copies them of what is in dx.
 template <int NE, bool F16> struct GradRing {
   using P = Parts<NE, F16>;
-  static constexpr int Slots = 8 + P::A + P::T + (F16 ? 1 : 0);   // 512 bytes each: x 4, dx 4, dl, scales
+  static constexpr int Slots = 8 + P::A + P::T + P::V;            // 512 bytes each: x 4, dx 4, dl, scales
   static constexpr int Stages = NE == 1 ? 3 : 2;                  // NE = 1: 17 KB a warp, 12 warps an SM
   static constexpr int Ring = 4 * Stages * Slots * 512;
   static constexpr int Sum = 4 * NE * 8 * 64 * 4;
@@ -542,7 +568,8 @@ __global__ void __launch_bounds__(128, NE == 4 ? 2 : 3) seq_grads_kernel(SeqBalA
     const uint4* fr = a.frag + (size_t)b * (P::A + P::T) * 32 + lane;
 #pragma unroll
     for (int i = 0; i < P::A + P::T; ++i) cp16(dst + i * 512, fr + i * 32, true);
-    if (F16) cp16(dst + (P::A + P::T) * 512, a.scales + (size_t)b * 8 + g, true);
+#pragma unroll
+    for (int i = 0; i < P::V; ++i) cp16(dst + (P::A + P::T + i) * 512, a.scales + ((size_t)b * 8 + g) * P::V + i, true);
   };
 #pragma unroll
   for (int st = 0; st < S; ++st)
@@ -583,8 +610,11 @@ __global__ void __launch_bounds__(128, NE == 4 ? 2 : 3) seq_grads_kernel(SeqBalA
     for (int i = 0; i < 4; ++i) xr[i] = slot(i);
 #pragma unroll
     for (int i = 0; i < P::A; ++i) A[i] = slot(8 + i);
-    float4 inv = make_float4(1.f, 1.f, 1.f, 0.f);
-    if (F16) inv = *reinterpret_cast<const float4*>(in + (8 + P::A + P::T) * 512);
+    DlScales<NE> inv;
+    if (F16) {
+      const float4* s = reinterpret_cast<const float4*>(in + (8 + P::A + P::T) * 512);
+      inv.load(s[0], s[32 * (P::V > 1)]);          // the second, where there is one, 512 bytes on
+    }
     // ---- dWg += dl^T x
     const uint32_t* xw[4] = {reinterpret_cast<const uint32_t*>(&xr[0]), reinterpret_cast<const uint32_t*>(&xr[1]),
                              reinterpret_cast<const uint32_t*>(&xr[2]), reinterpret_cast<const uint32_t*>(&xr[3])};
@@ -604,7 +634,8 @@ __global__ void __launch_bounds__(128, NE == 4 ? 2 : 3) seq_grads_kernel(SeqBalA
 #pragma unroll
         for (int i = TP - 1; i >= 0; --i) mma_16816<F16>(d4, At[i].x, At[i].y, At[i].z, At[i].w, p0, p1);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) acc[p][j][q] = F16 ? fmaf(d4[q], inv.z, acc[p][j][q]) : acc[p][j][q] + d4[q];
+        for (int q = 0; q < 4; ++q)
+          acc[p][j][q] = F16 ? fmaf(d4[q], inv.expert[NE == 1 ? 0 : 2 * p + (q >> 1)], acc[p][j][q]) : acc[p][j][q] + d4[q];
       }
     }
     // ---- dx (+)= dl Wg
@@ -640,8 +671,8 @@ __global__ void __launch_bounds__(128, NE == 4 ? 2 : 3) seq_grads_kernel(SeqBalA
             f0 = H::unpack(q0[i]);
             f1 = H::unpack(q1[i]);
           }
-          r0[i] = H::pack(fmaf(o0[2 * i], inv.x, f0.x), fmaf(o0[2 * i + 1], inv.x, f0.y));
-          r1[i] = H::pack(fmaf(o1[2 * i], inv.y, f1.x), fmaf(o1[2 * i + 1], inv.y, f1.y));
+          r0[i] = H::pack(fmaf(o0[2 * i], inv.row[0], f0.x), fmaf(o0[2 * i + 1], inv.row[0], f0.y));
+          r1[i] = H::pack(fmaf(o1[2 * i], inv.row[1], f1.x), fmaf(o1[2 * i + 1], inv.row[1], f1.y));
         }
         if (v0) __stcs(reinterpret_cast<uint4*>(dx + (size_t)t0 * D + 32 * h), make_uint4(r0[0], r0[1], r0[2], r0[3]));
         if (v1) __stcs(reinterpret_cast<uint4*>(dx + (size_t)t1 * D + 32 * h), make_uint4(r1[0], r1[1], r1[2], r1[3]));
@@ -878,7 +909,7 @@ seq_fused_kernel(const __grid_constant__ CUtensorMap tmap_x, const SeqBalArgs a,
 #pragma unroll
         for (int q = 0; q < 2; ++q) db[nt][q] += l[0][nt][q] + l[1][nt][q];
       uint4 fa[P::A], fw[P::T];
-      float4 scale;
+      DlScales<NE> scale;
       dl_fragments<NE, F16>(l, fa, fw, scale);
       const int use = j / kFuRouters;
       if (use > 0) {
@@ -890,7 +921,7 @@ seq_fused_kernel(const __grid_constant__ CUtensorMap tmap_x, const SeqBalArgs a,
       for (int i = 0; i < P::A; ++i) out[i * 32] = fa[i];
 #pragma unroll
       for (int i = 0; i < P::T; ++i) out[(P::A + i) * 32] = fw[i];
-      if (F16 && c == 0) reinterpret_cast<float4*>(slot + (P::A + P::T) * 512)[g] = scale;
+      if (F16 && c == 0) scale.store(reinterpret_cast<float4*>(slot + (P::A + P::T) * 512) + g);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&dl_full[w]));
     }
@@ -957,8 +988,11 @@ seq_fused_kernel(const __grid_constant__ CUtensorMap tmap_x, const SeqBalArgs a,
       uint4 At[P::T];
 #pragma unroll
       for (int i = 0; i < P::T; ++i) At[i] = reinterpret_cast<const uint4*>(slot)[(P::A + i) * 32 + lane];
-      float4 inv = make_float4(1.f, 1.f, 1.f, 0.f);
-      if (F16) inv = reinterpret_cast<const float4*>(slot + (P::A + P::T) * 512)[g];
+      DlScales<NE> inv;
+      if (F16) {
+        const float4 s = reinterpret_cast<const float4*>(slot + (P::A + P::T) * 512)[g];
+        inv.load(s, s);
+      }
       // rows of no sequence may hold anything: their x counts as zero (tokens 2c, 2c+1 and 2c+8, 2c+9)
       const bool whole = rb * 16 >= t_lo && rb * 16 + 16 <= t_hi;
       uint32_t k0 = 0xffffffffu, k1 = 0xffffffffu;
@@ -988,7 +1022,7 @@ seq_fused_kernel(const __grid_constant__ CUtensorMap tmap_x, const SeqBalArgs a,
               for (int i = P::T - 1; i >= 0; --i) mma_16816<F16>(d4, At[i].x, At[i].y, At[i].z, At[i].w, b[q][0], b[q][1]);
               float* s4 = acc[gi][2 * h + q];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) s4[k] = F16 ? fmaf(d4[k], inv.z, s4[k]) : s4[k] + d4[k];
+              for (int k = 0; k < 4; ++k) s4[k] = F16 ? fmaf(d4[k], inv.expert[NE == 1 ? 0 : k >> 1], s4[k]) : s4[k] + d4[k];
             }
           }
         }
@@ -1034,8 +1068,8 @@ seq_fused_kernel(const __grid_constant__ CUtensorMap tmap_x, const SeqBalArgs a,
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const float2 f0 = H::unpack(q0[i]), f1 = H::unpack(q1[i]);
-              r0[i] = H::pack(fmaf(o0[2 * i], inv.x, f0.x), fmaf(o0[2 * i + 1], inv.x, f0.y));
-              r1[i] = H::pack(fmaf(o1[2 * i], inv.y, f1.x), fmaf(o1[2 * i + 1], inv.y, f1.y));
+              r0[i] = H::pack(fmaf(o0[2 * i], inv.row[0], f0.x), fmaf(o0[2 * i + 1], inv.row[0], f0.y));
+              r1[i] = H::pack(fmaf(o1[2 * i], inv.row[1], f1.x), fmaf(o1[2 * i + 1], inv.row[1], f1.y));
             }
             if (v0) __stcs(reinterpret_cast<uint4*>(dx + (size_t)t0 * D + gi * 32), make_uint4(r0[0], r0[1], r0[2], r0[3]));
             if (v1) __stcs(reinterpret_cast<uint4*>(dx + (size_t)t1 * D + gi * 32), make_uint4(r1[0], r1[1], r1[2], r1[3]));
@@ -1432,6 +1466,10 @@ size_t seq_balance_frag_bytes(int E, int dtype) {
                 : E <= 16 ? (f16 ? Parts<2, true>::A + Parts<2, true>::T : Parts<2, false>::A + Parts<2, false>::T)
                           : (f16 ? Parts<4, true>::A + Parts<4, true>::T : Parts<4, false>::A + Parts<4, false>::T);
   return (size_t)n * 512;
+}
+
+size_t seq_balance_scale_bytes(int E, int dtype) {
+  return dtype != MOE_F16 ? 0 : (E <= 16 ? Parts<1, true>::V : Parts<4, true>::V) * 8 * sizeof(float4);
 }
 
 bool seq_balance_fused(int D, int E, int dtype) {
