@@ -1,5 +1,5 @@
 """moe_seq_balance where one call's values or shapes are at the ends of their range: experts that are hardly
-ever chosen."""
+ever chosen, every shape of the one-kernel form."""
 import numpy as np
 import pytest
 
@@ -45,3 +45,23 @@ def test_the_gate_row_of_a_rare_expert(T, D, E, low, dt):
     tol = (e.T @ np.abs(x) + gam * (a.T @ np.abs(x)))[rare]
     off = np.abs(o["dwg"].double().cpu().numpy() - dl.T @ x)[rare]
     assert np.all(off <= 1.01 * tol), (float((off / tol).max()), float(off.max()), float(np.abs(dl.T @ x)[rare].max()))
+
+
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("T,D,E,routing,off", [
+    (6001, 1152, 16, "race", [5, 700, 700, 3000, 5987]),   # one block of dx held; first and last rows inside a token block
+    (9000, 576, 9, "topk", [19, 4000, 8990]),
+    (8000, 1088, 12, "topk", [3, 4, 8000]),
+    (14300, 768, 8, "topk", [9, 7000, 14291]),             # the ring of x and both blocks of dx go round
+    (333, 1152, 16, "race", [17, 333]),
+    (14300, 512, 13, "race", [1, 14299]),
+    (7200, 1152, 1, "topk", [40, 41, 7199]),
+])
+def test_every_shape_of_the_one_kernel_form(T, D, E, routing, off, dt):
+    if dt == "f32" and E * D > 51200:
+        D = 64 * (51200 // E // 64)
+    c = Case(T, D, E, min(2, E), dt, routing, off, dead=np.nan)
+    c.check(c.run(aux=3.0), aux=3.0)
+    c.check(c.run(accumulate=False), accumulate=False)
+    o = c.run(dx=False)
+    c.check(o)
