@@ -437,7 +437,7 @@ int router_backward(const moe_config_t* cfg, const void* x, const void* wg, cons
   if ((uintptr_t)bws & 255u) return fail(MOE_ERR_INVALID_ARG, "bws must be 256-byte aligned");
   if (bws_bytes < moe_backward_workspace_size(cfg))
     return fail(MOE_ERR_WORKSPACE, "bws_bytes=%zu < %zu", bws_bytes, moe_backward_workspace_size(cfg));
-  if (dx_accumulate && !dx) return fail(MOE_ERR_INVALID_ARG, "dx_accumulate needs dx");
+  if (dx_accumulate && !dx && cfg->T > 0) return fail(MOE_ERR_INVALID_ARG, "dx_accumulate needs dx");
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e;
   if (cfg->T == 0) {
@@ -1165,10 +1165,11 @@ int moe_seq_balance(const moe_config_t* cfg, const void* x, const void* wg, cons
   if (!seq_offsets && (long long)n_seqs * seq_len != cfg->T)
     return fail(MOE_ERR_INVALID_ARG, "n_seqs=%d images of %d tokens are not T=%d", n_seqs, seq_len, cfg->T);
   if (!dwg && (dbias || dx || dgate)) return fail(MOE_ERR_INVALID_ARG, "dbias, dx and dgate need dwg");
-  if (dx_accumulate && !dx) return fail(MOE_ERR_INVALID_ARG, "dx_accumulate needs dx");
+  if (dx_accumulate && !dx && cfg->T > 0) return fail(MOE_ERR_INVALID_ARG, "dx_accumulate needs dx");
   if (dx && dx == x) return fail(MOE_ERR_INVALID_ARG, "dx and x are one buffer");
   if (!std::isfinite(aux_scale)) return fail(MOE_ERR_INVALID_ARG, "aux_scale=%g", aux_scale);
-  if (cfg->routing == MOE_ROUTE_RACE && !n_sel) return fail(MOE_ERR_INVALID_ARG, "n_sel is required for Expert-Race routing");
+  if (cfg->routing == MOE_ROUTE_RACE && !n_sel && cfg->T > 0)
+    return fail(MOE_ERR_INVALID_ARG, "n_sel is required for Expert-Race routing");
   if (n_seqs > 0) {
     REQUIRE_PTR(seq_counts);
     REQUIRE_PTR(seq_loss);
