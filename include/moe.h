@@ -482,16 +482,18 @@ int moe_expert_frequency(const moe_config_t* cfg, const int32_t* topk_idx, const
  *   x, wg, router_bias   as given to moe_route (the scores are recomputed in fp32)
  *   seq_offsets [n_seqs+1] int32 ascending, 0..T: sequence b is rows seq_offsets[b] ..
  *               seq_offsets[b+1]-1 and may be empty.  NULL: images of cfg->seq_len rows each (0: the
- *               whole call is one), n_seqs = T / seq_len.  Rows of no sequence take no part: their
- *               x may hold anything and their rows of dx stay as they are.
+ *               whole call is one), n_seqs = T / seq_len.  Rows of no sequence take no part (but see
+ *               flags): their x may hold anything and their rows of dx stay as they are.
  *   topk_idx, n_sel      from moe_route (n_sel NULL: K slots for every token)
  *   dgate       [T,Kmax] fp32 from moe_expert_backward, or NULL
  *   aux_scale   dJ/dloss
  *   seq_counts  [n_seqs,E] int32 out: selected pairs of each sequence and expert
  *   seq_loss    [n_seqs] fp32 out; loss [1] fp32 out
  *   dwg         [E,D] fp32 out, or NULL for the loss and the counts alone (then dbias and dx too)
- *   dbias       [E] fp32 out or NULL; dx [T,D] act out or NULL, not x; dx_accumulate 1: dx += the
- *               router's part
+ *   dbias       [E] fp32 out or NULL; dx [T,D] act out or NULL, not x
+ *   flags       0, or of moe_seq_balance_flags_t: dx += the router's part; rows of no sequence take part
+ *               with their gates' gradient, as in the gradient of a loss of every row's output to which
+ *               the balance of some is added (x and topk_idx of those rows are then read, their dx written)
  *   bws         scratch of moe_seq_balance_workspace_size(cfg, n_seqs) bytes, 256-byte aligned
  *   ws          status word only: offsets that descend or leave 0..T, or an expert id >= E (which is
  *               skipped), are reported through moe_check_status
@@ -499,11 +501,13 @@ int moe_expert_frequency(const moe_config_t* cfg, const int32_t* topk_idx, const
  * 22 bits below the expert's own largest of 16 consecutive tokens (fp16), and dx as 16 bits, or 22 below
  * its token's largest; sums are fp32.
  */
+typedef enum { MOE_SEQ_DX_ACCUMULATE = 1, MOE_SEQ_ALL_GATES = 2 } moe_seq_balance_flags_t;
+
 size_t moe_seq_balance_workspace_size(const moe_config_t* cfg, int32_t n_seqs);
 int moe_seq_balance(const moe_config_t* cfg, const void* x, const void* wg, const float* router_bias,
                     const int32_t* seq_offsets, int32_t n_seqs, const int32_t* topk_idx, const int32_t* n_sel,
                     const float* dgate, float aux_scale, int32_t* seq_counts, float* seq_loss, float* loss, float* dwg,
-                    float* dbias, void* dx, int32_t dx_accumulate, void* bws, size_t bws_bytes, void* ws, void* stream);
+                    float* dbias, void* dx, int32_t flags, void* bws, size_t bws_bytes, void* ws, void* stream);
 
 /*
  * The optimizer: AdamW over many tensors at once, with the gradient norm it clips by (the pages

@@ -20,6 +20,7 @@ MOE_ERR_CUDA, MOE_ERR_DEVICE_CHECK, MOE_ERR_TIMEOUT = -4, -5, -6
 MOE_F32, MOE_BF16, MOE_F16 = 0, 1, 2
 MOE_ROUTE_TOPK, MOE_ROUTE_RACE = 0, 1
 MOE_MOMENTS_F32, MOE_MOMENTS_E4M3 = 0, 1
+MOE_SEQ_DX_ACCUMULATE, MOE_SEQ_ALL_GATES = 1, 2
 MOE_GEMM_AUTO, MOE_GEMM_SIMT, MOE_GEMM_TC1 = 0, 1, 2
 
 
@@ -315,11 +316,13 @@ def moe_seq_balance_workspace_size(cfg, n_seqs) -> int:
 
 
 def moe_seq_balance(cfg, x, wg, router_bias, seq_offsets, n_seqs, topk_idx, n_sel, dgate, aux_scale, seq_counts, seq_loss,
-                    loss, dwg, dbias, dx, dx_accumulate, bws, bws_bytes, ws, stream=0):
-    """Balance loss per packed sequence, its counts and (dwg given) its and the gates' gradient through the router."""
+                    loss, dwg, dbias, dx, dx_accumulate, bws, bws_bytes, ws, stream=0, all_gates=0):
+    """Balance loss per packed sequence, its counts and (dwg given) its and the gates' gradient through the router
+    (all_gates: of rows of no sequence too)."""
+    flags = (MOE_SEQ_DX_ACCUMULATE if dx_accumulate else 0) | (MOE_SEQ_ALL_GATES if all_gates else 0)
     _check(lib.moe_seq_balance(C.byref(cfg), _ptr(x), _ptr(wg), _ptr(router_bias), _ptr(seq_offsets), n_seqs,
                                _ptr(topk_idx), _ptr(n_sel), _ptr(dgate), aux_scale, _ptr(seq_counts), _ptr(seq_loss),
-                               _ptr(loss), _ptr(dwg), _ptr(dbias), _ptr(dx), dx_accumulate, _ptr(bws), bws_bytes, _ptr(ws),
+                               _ptr(loss), _ptr(dwg), _ptr(dbias), _ptr(dx), flags, _ptr(bws), bws_bytes, _ptr(ws),
                                stream))
 
 

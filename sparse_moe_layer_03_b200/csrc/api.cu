@@ -1158,13 +1158,16 @@ size_t moe_seq_balance_workspace_size(const moe_config_t* cfg, int32_t n_seqs) {
 int moe_seq_balance(const moe_config_t* cfg, const void* x, const void* wg, const float* router_bias,
                     const int32_t* seq_offsets, int32_t n_seqs, const int32_t* topk_idx, const int32_t* n_sel,
                     const float* dgate, float aux_scale, int32_t* seq_counts, float* seq_loss, float* loss, float* dwg,
-                    float* dbias, void* dx, int32_t dx_accumulate, void* bws, size_t bws_bytes, void* ws, void* stream) {
+                    float* dbias, void* dx, int32_t flags, void* bws, size_t bws_bytes, void* ws, void* stream) {
   int rc = check_seqs(cfg, n_seqs);
   if (rc) return rc;
+  if (flags & ~(MOE_SEQ_DX_ACCUMULATE | MOE_SEQ_ALL_GATES)) return fail(MOE_ERR_INVALID_ARG, "flags=%d", flags);
+  const bool dx_accumulate = flags & MOE_SEQ_DX_ACCUMULATE, all_gates = flags & MOE_SEQ_ALL_GATES;
   const int seq_len = cfg->seq_len > 0 ? cfg->seq_len : cfg->T;
   if (!seq_offsets && (long long)n_seqs * seq_len != cfg->T)
     return fail(MOE_ERR_INVALID_ARG, "n_seqs=%d images of %d tokens are not T=%d", n_seqs, seq_len, cfg->T);
   if (!dwg && (dbias || dx || dgate)) return fail(MOE_ERR_INVALID_ARG, "dbias, dx and dgate need dwg");
+  if (all_gates && !dgate && cfg->T > 0) return fail(MOE_ERR_INVALID_ARG, "MOE_SEQ_ALL_GATES needs dgate");
   if (dx_accumulate && !dx && cfg->T > 0) return fail(MOE_ERR_INVALID_ARG, "dx_accumulate needs dx");
   if (dx && dx == x) return fail(MOE_ERR_INVALID_ARG, "dx and x are one buffer");
   if (!std::isfinite(aux_scale)) return fail(MOE_ERR_INVALID_ARG, "aux_scale=%g", aux_scale);
@@ -1204,9 +1207,9 @@ int moe_seq_balance(const moe_config_t* cfg, const void* x, const void* wg, cons
   a.T = cfg->T; a.D = cfg->D; a.E = cfg->E; a.K = cfg->K; a.Kmax = kmax_of(cfg); a.dtype = cfg->dtype;
   a.factor = (float)((double)cfg->alpha * cfg->E / cfg->K); a.aux_scale = aux_scale;
   a.offsets = seq_offsets; a.n_seqs = n_seqs; a.seq_len = seq_len;
-  a.topk_idx = topk_idx; a.n_sel = n_sel; a.dgate = dgate;
+  a.topk_idx = topk_idx; a.n_sel = n_sel; a.dgate = dgate; a.all_gates = all_gates;
   a.counts = seq_counts; a.seq_loss = seq_loss; a.loss = loss;
-  a.grads = dwg != nullptr; a.dwg = dwg; a.dbias = dbias; a.dx = dx; a.accumulate = dx_accumulate != 0;
+  a.grads = dwg != nullptr; a.dwg = dwg; a.dbias = dbias; a.dx = dx; a.accumulate = dx_accumulate;
   seq_balance_plan(cfg->T, cfg->D, cfg->E, cfg->dtype, &a.groups, &a.blocks_per_range);
   a.live = ws_at<int>(bws, L.live);
   a.tok = ws_at<int2>(bws, L.tok);

@@ -285,6 +285,7 @@ struct SeqBalArgs {
   const int32_t* offsets; int n_seqs, seq_len;        // [n_seqs + 1] row borders, or null: seq_len rows each
   const int32_t* topk_idx; const int32_t* n_sel;      // n_sel null: K slots each
   const float* dgate;                                 // [T,Kmax] or null
+  int all_gates;                                      // dgate of rows of no sequence counts too
   int32_t* counts; float* seq_loss; float* loss;      // outputs [n_seqs,E], [n_seqs], [1]
   int grads;                                          // the gradients below are wanted
   float* dwg; float* dbias; void* dx; int accumulate; // dbias and dx may be null

@@ -9,7 +9,7 @@
 //     dl = P (dP - sum_j P dP),   dWg = dl^T x,   db = sum_t dl,   dx (+)= dl Wg.
 // A token's share of its sequence's loss, sum_i P[t,i] C[b,i] with C = alpha E c / (K L_b^2),
 // is a by-product of the softmax's backward.  Rows of no sequence take no part, whatever their
-// x holds, and their dx stays.
+// x holds, and their dx stays; or, with all_gates, the part that their own dgate gives them (C = 0).
 //
 // The launches, chained by programmatic dependent launch:
 //   count   sequence and factor of every token, counts (integer atomics; cleared before, where many)
@@ -59,10 +59,11 @@ __device__ __forceinline__ float quad_max(float v) {
   v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
   return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
 }
-// first and one past the last row that belong to a sequence
+// first and one past the last row that take part: those of the sequences, or all
 __device__ __forceinline__ void live_rows(const SeqBalArgs& a, int& lo, int& hi) {
-  lo = a.offsets ? min(max(a.offsets[0], 0), a.T) : 0;
-  hi = a.offsets ? min(max(a.offsets[a.n_seqs], lo), a.T) : a.T;
+  const bool some = a.offsets && !a.all_gates;
+  lo = some ? min(max(a.offsets[0], 0), a.T) : 0;
+  hi = some ? min(max(a.offsets[a.n_seqs], lo), a.T) : a.T;
 }
 __device__ __forceinline__ int slots_of(const SeqBalArgs& a, int t) {
   return a.n_sel ? min(max(a.n_sel[t], 0), a.Kmax) : a.K;
@@ -152,12 +153,12 @@ __global__ void __launch_bounds__(ONE ? kOneThreads : kCountThreads) seq_count_k
         const float coef = sid >= 0 ? a.factor / ((float)len * (float)len) : 0.f;
         a.tok[t] = make_int2(sid, __float_as_int(coef));
       }
-      const int use = sid >= 0 ? ns[i] : 0;
+      const int use = sid >= 0 || a.all_gates ? ns[i] : 0;
       auto add = [&](int k, int e) {               // every lane, for __match_any_sync
         long long key = -1;
         if (k < use) {
           if (e >= a.E) set_status(a.status, DEV_BAD_INDEX, 411);
-          else if (e >= 0) key = (long long)sid * a.E + e;
+          else if (e >= 0 && sid >= 0) key = (long long)sid * a.E + e;
         }
         if (ONE) {
           if (key >= 0) atomicAdd(&hist[key], 1);
@@ -277,20 +278,20 @@ __device__ __forceinline__ void scatter_gates(const SeqBalArgs& a, const GatesAh
 // What a lane holds of a block: rows t0 = 16 rb + g and t0 + 8 (r = 0, 1), experts nt * 8 + 2c + q.
 template <int NE> using RowPair = float[2][NE][2];
 
-// C = factor * counts of the rows' sequences
+// C = factor * counts of the rows' sequences; in: the row takes part
 template <int NE>
 __device__ __forceinline__ void load_counts(const SeqBalArgs& a, const bool* live, int t0, RowPair<NE>& C, bool* in) {
   const int c = threadIdx.x & 3;
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     const int2 tk = live[r] ? a.tok[t0 + 8 * r] : make_int2(-1, 0);
-    in[r] = tk.x >= 0;
+    in[r] = tk.x >= 0 || (live[r] && a.all_gates);
 #pragma unroll
     for (int nt = 0; nt < NE; ++nt)
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         const int e = nt * 8 + 2 * c + q;
-        C[r][nt][q] = in[r] && e < a.E ? __int_as_float(tk.y) * (float)a.counts[(size_t)tk.x * a.E + e] : 0.f;
+        C[r][nt][q] = tk.x >= 0 && e < a.E ? __int_as_float(tk.y) * (float)a.counts[(size_t)tk.x * a.E + e] : 0.f;
       }
   }
 }
@@ -1186,7 +1187,7 @@ __global__ void __launch_bounds__(TOK == 2 ? 256 : 128) seq_scores_f32_kernel(Se
 #pragma unroll
   for (int i = 0; i < TOK; ++i) {
     const int t = tb + i;
-    const int2 tk = tok[i];
+    const bool in = tok[i].x >= 0 || (a.all_gates && t < a.T);
     float mine = -INFINITY;
 #pragma unroll
     for (int e = 0; e < EP; ++e)
@@ -1200,7 +1201,7 @@ __global__ void __launch_bounds__(TOK == 2 ? 256 : 128) seq_scores_f32_kernel(Se
     for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
     const float P = pe * (1.0f / z);
     float dp = aux * C[i];
-    const int ns = tk.x >= 0 ? slots[i] : 0;       // the same in every lane
+    const int ns = in ? slots[i] : 0;              // the same in every lane
     for (int k = 0; k < ns; ++k) {
       const int e = __shfl_sync(0xffffffffu, sel[i], k);
       const float v = __shfl_sync(0xffffffffu, gate[i], k);
@@ -1212,8 +1213,8 @@ __global__ void __launch_bounds__(TOK == 2 ? 256 : 128) seq_scores_f32_kernel(Se
       share += __shfl_xor_sync(0xffffffffu, share, o);
       pc += __shfl_xor_sync(0xffffffffu, pc, o);
     }
-    share = tk.x >= 0 ? share : 0.f;
-    const float dl = tk.x >= 0 && lane < E ? P * (dp - pc) : 0.f;
+    share = in ? share : 0.f;
+    const float dl = in && lane < E ? P * (dp - pc) : 0.f;
     if (t < a.T) {
       if (lane == 0) a.tok_loss[t] = share;
       if (a.grads && lane < EP) a.dl[(size_t)t * EP + lane] = dl;

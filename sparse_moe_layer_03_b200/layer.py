@@ -240,14 +240,16 @@ class MoELayer:
 
     # ------------------------------------------------------------ backward
     def seq_balance(self, x: torch.Tensor, seq_offsets: Optional[torch.Tensor] = None,
-                    dgate: Optional[torch.Tensor] = None, aux_scale: float = 1.0, grads: Optional[dict] = None) -> dict:
+                    dgate: Optional[torch.Tensor] = None, aux_scale: float = 1.0, grads: Optional[dict] = None,
+                    all_gates: bool = False) -> dict:
         """The last routing's balance loss per packed sequence: ``balance_loss`` [1] (the mean over the
         sequences that hold a token), ``seq_loss`` [n] and ``seq_counts`` [n, E].
 
         ``seq_offsets`` [n + 1] (int32, on the device): sequence b is rows seq_offsets[b] ..
         seq_offsets[b+1]-1 of ``x``; rows of no sequence take no part.  Without it, images of the shape's
         ``seq_len`` tokens.  ``grads`` (a dict with dwg, dbias, dx) receives the router's gradients of
-        aux_scale * balance_loss, with those of the gates ``dgate``; its dx is added to."""
+        aux_scale * balance_loss, with those of the gates ``dgate``; its dx is added to.  ``all_gates``: the
+        gates of rows of no sequence count too (their x is read and their dx added to)."""
         s, dev = self.s, self.device
         g = grads or {}
         f32, T = torch.float32, self.cfg.T
@@ -273,7 +275,7 @@ class MoELayer:
         B.moe_seq_balance(self.cfg, x, self.wg, self.router_bias, seq_offsets, n, self.topk_idx, self.n_sel, dgate,
                           aux_scale, out["seq_counts"], out["seq_loss"], out["balance_loss"], g.get("dwg"),
                           g.get("dbias"), g.get("dx"), int(g.get("dx") is not None), self._sbws, self._sbws.numel(),
-                          self.ws, self.stream())
+                          self.ws, self.stream(), all_gates=int(all_gates))
         return out
 
     def backward(self, x: torch.Tensor, dout: torch.Tensor, aux_scale: float = 1.0,
@@ -286,8 +288,8 @@ class MoELayer:
         default dispatch, not the gathered GEMM1).
 
         With the shape's ``seq_len``, or ``seq_offsets`` [n + 1] (see ``seq_balance``), L_balance is the
-        mean over sequences, and ``balance_loss``, ``seq_loss`` and ``seq_counts`` are returned too; the
-        gates of rows that belong to no sequence then carry no gradient to the router."""
+        mean over sequences, and ``balance_loss``, ``seq_loss`` and ``seq_counts`` are returned too.  Rows
+        that belong to no sequence are still rows of MoE(x): dout is 0 where they are padding."""
         if self.x_perm is None:
             raise ValueError("the backward reads x_perm: run the forward without gather_rows")
         s, dev, T = self.s, self.device, self.cfg.T
@@ -311,7 +313,7 @@ class MoELayer:
                               self.row_token, self.row_gate, wts, self.h_perm, self.h_sh, dout, grads, g["dgate"],
                               g["dx"], self.ws, self.ws_bytes, self._ebws, self._ebws_bytes, self.stream())
         if s.seq_len or seq_offsets is not None:
-            g.update(self.seq_balance(x, seq_offsets, g["dgate"], aux_scale, g))
+            g.update(self.seq_balance(x, seq_offsets, g["dgate"], aux_scale, g, all_gates=True))
             return g
         B.moe_router_backward(self.cfg, x, self.wg, self.router_bias, self.counts, self.topk_idx, self.n_sel,
                               g["dgate"], aux_scale, g["dwg"], g["dbias"], g["dx"], 1, self._rbws, self._rbws_bytes,

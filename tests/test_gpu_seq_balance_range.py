@@ -1,5 +1,5 @@
 """moe_seq_balance where one call's values or shapes are at the ends of their range: experts that are hardly
-ever chosen, every shape of the one-kernel form, no tokens."""
+ever chosen, every shape of the one-kernel form, no tokens, rows of no sequence that carry their gates' gradient."""
 import numpy as np
 import pytest
 import torch
@@ -113,3 +113,79 @@ def test_a_layer_without_tokens(seq_len, offsets, routing):
     assert g["dx"].shape == (0, 64)
     if seq_len or offsets:
         assert float(g["balance_loss"]) == 0.0
+
+
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("T,D,E,routing,off", [
+    (700, 256, 8, "topk", [0, 300, 612]), (333, 128, 16, "race", [17, 40, 333]), (400, 192, 24, "topk", [399, 400]),
+    (5001, 768, 8, "topk", [9, 2000, 4991]), (2500, 1152, 16, "race", [5, 2000]), (5001, 128, 20, "topk", [33, 4000]),
+    (6000, 64, 4, "topk", [0, 3001]), (90, 64, 4, "topk", [7, 7]), (300, 512, 2, "topk", [300, 300])])
+def test_gates_of_every_row(T, D, E, routing, off, dt):
+    c = Case(T, D, E, 2, dt, routing, off)
+    held = []
+    for acc in (True, False):
+        o = c.run(aux=3.0, accumulate=acc, hold=held)
+        o["dx"].copy_(torch.as_tensor(c.old).to(DEV, TYPES[dt]))
+        args = held[-1]
+        st = torch.cuda.current_stream().cuda_stream
+        B.moe_seq_balance(*args, st, all_gates=1)
+        B.moe_check_status(args[-1], st)
+        live = c.live.copy()
+        c.live[:] = True
+        c.check(o, aux=3.0, accumulate=acc)
+        c.live = live
+    # an expert out of range is reported in any row
+    if not c.live.all():
+        idx = args[6].clone()
+        idx[int(np.nonzero(~c.live & (c.n_sel > 0))[0][0]), 0] = E
+        args = args[:6] + (idx,) + args[7:]
+        B.moe_seq_balance(*args, st, all_gates=1)
+        with pytest.raises(B.MoeError, match="bad index"):
+            B.moe_check_status(args[-1], st)
+
+
+def test_gates_of_every_row_where_all_belong_to_sequences():
+    # the flag changes nothing: the same bits
+    c = Case(1000, 768, 8, 2, "bf16", offsets=[0, 400, 1000])
+    held = []
+    o = c.run(hold=held)
+    want = {k: v.clone() for k, v in o.items()}
+    o["dx"].copy_(torch.as_tensor(c.old).to(DEV, torch.bfloat16))
+    B.moe_seq_balance(*held[0], torch.cuda.current_stream().cuda_stream, all_gates=1)
+    torch.cuda.synchronize()
+    for k in want:
+        assert torch.equal(want[k], o[k]), k
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("routing", ["topk", "race"])
+def test_a_layers_rows_of_no_sequence_keep_their_gates_gradient(dt, routing):
+    # J = <dout, MoE(x)> + aux L with L over some of the rows: the first term is every row's
+    from sparse_moe_layer_03_b200.layer import LayerShape, MoELayer
+    T = 512
+    w = I.small_workload(T, 256, 512, 8, 2, 1, dt, routing, seed=23)
+    inp = I.make_inputs(w, bias_std=0.1)
+    layer = MoELayer(LayerShape(w.T, w.D, w.H, w.E, w.K, w.n_shared, w.dtype, w.routing, w.alpha), inp)
+    x = torch.as_tensor(inp["x"]).to(DEV, layer.act_dtype)
+    off = [101, 200, 200, 390]
+    off_d = torch.tensor(off, dtype=torch.int32, device=DEV)
+    # the rows outside matter most, so that leaving them out is far beyond the bound
+    d = np.random.default_rng(2).standard_normal((T, w.D))
+    d[off[0]:off[-1]] *= 0.1
+    dout = I._store(d, dt)
+    layer.forward(x)
+    g = layer.backward(x, torch.as_tensor(dout).to(DEV, layer.act_dtype), aux_scale=50.0, seq_offsets=off_d)
+    torch.cuda.synchronize()
+    layer.check()
+    idx = PA.gpu_selection(PA.fetch(layer))
+    P = O.softmax_scores(O.gate_logits(inp["x"], inp["wg"], inp.get("router_bias")))
+    loss, per, counts, dP = O.balance_packed(idx, P, w.K, w.alpha, off)
+    assert np.array_equal(g["seq_counts"].cpu().numpy(), counts)
+    assert abs(float(g["balance_loss"]) - loss) <= 1e-4 * loss
+    ref = O.layer_backward(inp, idx, dout, w.K, w.alpha, aux_scale=0.0)
+    add = O.router_backward(inp["x"], inp["wg"], 50.0 * O.softmax_backward(P, dP))
+    ref["dwg"], ref["dbias"], ref["dx"] = ref["dwg"] + add[0], ref["dbias"] + add[1], ref["dx"] + add[2]
+    for n in ("dwg", "dbias", "dx", "dw1", "dw2"):
+        assert PA.rel_err(g[n].float().cpu().numpy(), ref[n]) <= PA.out_tol(w), n
+    rows = np.r_[0:off[0], off[-1]:T]
+    assert PA.rel_err(g["dx"].float().cpu().numpy()[rows], ref["dx"][rows]) <= PA.out_tol(w)
