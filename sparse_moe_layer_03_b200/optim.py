@@ -227,12 +227,16 @@ class AdamW(_Control):
         B.moe_adamw_step(settings, tensors, n, self._ctl_ptr, stream)
 
     def state_dict(self) -> dict:
-        """Copies of the state and the step count (waits for the device)."""
+        """Copies of the state and the step count: of all steps issued before, on any stream, and of none
+        issued later (waits for the device, and for the copies)."""
         step = self.steps_taken()
-        return dict({k: b.clone() for k, b in self.buffers.items()}, step=step)
+        state = dict({k: b.clone() for k, b in self.buffers.items()}, step=step)
+        torch.cuda.synchronize(self.device)
+        return state
 
     def load_state_dict(self, state: dict):
-        """Take up a ``state_dict``.  ``lr_scale`` is 1 and ``skipped`` 0 again."""
+        """Take up a ``state_dict``, behind all steps issued before and ahead of all issued later (waits for the
+        device on both sides).  ``lr_scale`` is 1 and ``skipped`` 0 again."""
         if set(state) != set(self.buffers) | {"step"}:
             raise ValueError(f"state has {sorted(state)}, not {sorted(self.buffers) + ['step']}")
         for k, b in self.buffers.items():
@@ -240,9 +244,11 @@ class AdamW(_Control):
                 raise ValueError(f"state[{k!r}] is {tuple(state[k].shape)} {state[k].dtype}, not {tuple(b.shape)} {b.dtype}")
         if int(state["step"]) < 0:
             raise ValueError(f"state['step'] is {state['step']}")
+        torch.cuda.synchronize(self.device)
         for k, b in self.buffers.items():
             b.copy_(state[k])
         self._init(int(state["step"]), self.betas)
+        torch.cuda.synchronize(self.device)
 
 
 class LayerAdamW(AdamW):
@@ -271,7 +277,9 @@ class LayerAdamW(AdamW):
 
     def state_dict(self) -> dict:
         """Copies of the state, the step count and the masters (waits for the device)."""
-        return dict(super().state_dict(), params=[p.clone() for p in self.params])
+        state = dict(super().state_dict(), params=[p.clone() for p in self.params])
+        torch.cuda.synchronize(self.device)
+        return state
 
     def load_state_dict(self, state: dict):
         """Take up a ``state_dict``: the layer's weights become those of its masters."""
@@ -284,3 +292,4 @@ class LayerAdamW(AdamW):
             p.copy_(saved)
             if w is not None:
                 w.copy_(p)
+        torch.cuda.synchronize(self.device)
