@@ -17,6 +17,7 @@ import torch
 
 from . import binding as B
 
+ALIGN = 16             # bytes: the kernels' vectors start at each tensor's first element
 BLOCK = 256            # elements that share a scale of 8-bit moments; each tensor's state starts on such a block
 _DTYPE = {torch.float32: B.MOE_F32, torch.bfloat16: B.MOE_BF16, torch.float16: B.MOE_F16}
 
@@ -32,6 +33,8 @@ def _check(t, what, dtypes, device, n=None):
         raise ValueError(f"{what} is on {t.device}, not on {device}")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
+    if t.numel() and t.data_ptr() % ALIGN:
+        raise ValueError(f"{what} starts at an address that is not {ALIGN}-byte aligned")
     if n is not None and t.numel() != n:
         raise ValueError(f"{what} has {t.numel()} elements, not {n}")
 
@@ -97,12 +100,15 @@ class _GradList:
                 _check(g, f"grads[{i}]", tuple(_DTYPE), device, None if sizes is None else sizes[i])
             new = (g.data_ptr(), n, dt)
             if held[i] != new:
+                if new[0] % ALIGN:
+                    _check(g, f"grads[{i}]", tuple(_DTYPE), device)
                 t = self.items[i]
                 t.grad, t.n, t.grad_dtype = held[i] = new
 
 
 class GradNorm(_Control):
-    """2-norm of a list of gradients (fp32, bf16 or fp16) together, and the factor that clips them.
+    """2-norm of a list of gradients (fp32, bf16 or fp16; contiguous, 16-byte aligned) together, and the factor
+    that clips them.
 
     ``norm, scale = GradNorm(device)(grads, max_norm=1.0)``: views of the control block, [1] fp32 each,
     overwritten by the next call.  ``scale`` is 0 and ``nonfinite`` 1 where a gradient is not finite."""
@@ -122,7 +128,8 @@ class GradNorm(_Control):
 
 
 class AdamW(_Control):
-    """AdamW over many tensors in one launch.
+    """AdamW over many tensors in one launch.  Every tensor is contiguous and starts at a 16-byte aligned
+    address (slices of a flat buffer: at a multiple of 16 bytes); others are refused.
 
     ``params``: fp32 tensors, updated in place.  ``weights``: for each its bf16 or fp16 copy, which
     every step rewrites, or None.  ``weight_decay``: one value or one for each tensor.  ``state``:

@@ -1,4 +1,4 @@
-"""An optimizer's state taken and restored while other streams step it."""
+"""An optimizer's state taken and restored while other streams step it, and tensors that the vectors do not fit."""
 import pytest
 import torch
 
@@ -99,3 +99,20 @@ def test_a_step_right_behind_load_state_dict_starts_from_it(make):
     for a, b in zip(want, _all(opt)):
         assert torch.equal(a, b)
     assert opt.steps_taken() == 2
+
+
+@pytest.mark.parametrize("what", ["params", "weights", "grads", "norm"])
+def test_tensors_off_the_vectors_are_refused_by_name(what):
+    p, odd = torch.zeros(64, device=DEV), torch.zeros(65, device=DEV)[1:]
+    with pytest.raises(ValueError, match="16-byte aligned"):
+        if what == "params":
+            optim.AdamW([p, odd], lr=1e-3)
+        elif what == "weights":
+            optim.AdamW([p], [torch.zeros(65, dtype=torch.half, device=DEV)[1:]], lr=1e-3)
+        elif what == "grads":
+            optim.AdamW([p], lr=1e-3).step([odd])
+        else:
+            optim.GradNorm(DEV)([p, odd])
+    # nothing there, nothing to align
+    optim.AdamW([p, odd[:0]], lr=1e-3).step([p, odd[:0]], max_norm=1.0)
+    torch.cuda.synchronize()
