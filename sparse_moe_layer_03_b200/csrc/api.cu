@@ -1137,8 +1137,7 @@ static SbLayout sb_layout(const moe_config_t* c) {
   L.frag = take(is16(c) ? nblk * seq_balance_frag_bytes(c->E, c->dtype) : 0);
   L.scales = take(nblk * seq_balance_scale_bytes(c->E, c->dtype));
   L.dl = take(is16(c) ? 0 : T * ep * 4);
-  // rows of the two kernels' token blocks, or four router warps of each block of the fused one
-  L.db_part = take((nblk > 4 * (size_t)groups ? nblk : 4 * (size_t)groups) * ep * 4);
+  L.db_part = take((size_t)seq_balance_db_rows(c->T, c->D, c->E, c->dtype, groups) * ep * 4);
   L.partials = take((size_t)groups * c->E * c->D * 4);
   L.total = off;
   return L;

@@ -300,7 +300,7 @@ struct SeqBalArgs {
   uint4* frag;                                        // 16-bit: dl in fragment order, seq_balance_frag_bytes a block
   float4* scales;                                     // fp16: inverse scales, seq_balance_scale_bytes a block
   float* dl;                                          // fp32: [T, ep]
-  float* db_part;                                     // [blocks, ep] sums of dl over blocks of tokens
+  float* db_part;                                     // [seq_balance_db_rows, ep] sums of dl over tokens
   float* partials;                                    // [groups, E, D]
   int* status;
 };
@@ -311,6 +311,7 @@ size_t seq_balance_frag_bytes(int E, int dtype);
 size_t seq_balance_scale_bytes(int E, int dtype);
 bool seq_balance_fused(int D, int E, int dtype);      // else the shape takes the two kernels
 void seq_balance_plan(int T, int D, int E, int dtype, int* groups, int* blocks_per_range);
+int seq_balance_db_rows(int T, int D, int E, int dtype, int groups);   // sums of dl that the gradients leave for db
 cudaError_t launch_seq_balance(const SeqBalArgs& a, cudaStream_t s);
 
 // ---- optim.cu: gradient norm and AdamW over many tensors

@@ -1495,6 +1495,11 @@ void seq_balance_plan(int T, int D, int E, int dtype, int* groups, int* blocks_p
   *groups = (ranges + 3) / 4;
 }
 
+// one from each router warp of the one kernel, or from each 16 tokens of the two
+int seq_balance_db_rows(int T, int D, int E, int dtype, int groups) {
+  return seq_balance_fused(D, E, dtype) ? groups * kFuRouters : (T + 15) / 16;
+}
+
 cudaError_t launch_seq_balance(const SeqBalArgs& a, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   if (a.T <= kOneTokens && (long long)a.n_seqs * a.E <= kOneCounts && a.n_seqs < kOffSmem) {
@@ -1515,7 +1520,7 @@ cudaError_t launch_seq_balance(const SeqBalArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int wg_blocks = a.dwg ? a.E * a.D / 32 : 0, db_blocks = a.dbias ? a.E : 0;
   const bool one = a.dtype == MOE_F32 && a.T <= kSbF32Single;   // db and the losses token by token
-  const int db_rows = one ? a.T : a.fused ? a.groups * kFuRouters : (a.T + 15) / 16;
+  const int db_rows = one ? a.T : seq_balance_db_rows(a.T, a.D, a.E, a.dtype, a.groups);
   return chained<seq_finish_kernel, 0>(wg_blocks + db_blocks + a.n_seqs + 1, kFinThreads, 0, s, a,
                  (const float*)(one ? a.dl : a.db_part), db_rows, seq_balance_ep(a.E), wg_blocks, db_blocks);
 }

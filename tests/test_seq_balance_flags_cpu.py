@@ -39,3 +39,17 @@ def test_every_rows_gates_and_some_rows_balance(offsets):
     J.backward()
     for got, want in zip((dx, dwg, db), args):
         np.testing.assert_allclose(got, want.grad.numpy(), rtol=1e-9, atol=1e-13)
+
+
+def test_the_workspace_holds_each_forms_parts():
+    # by part, each rounded up to 256 bytes: tokens' sequences and losses, blocks' losses, and of the form that
+    # the shape takes the sums of dl for dbias (3 router warps in each of up to 148 blocks, or one of each 16
+    # tokens), dl's fragments and the partial sums of dWg
+    up = lambda n: -(-max(n, 1) // 256) * 256  # noqa: E731
+    for T in (1, 100, 3000, 32768):
+        nblk = -(-T // 16)
+        groups = min(nblk, 148)
+        got = B.moe_seq_balance_workspace_size(B.make_config(T, 1152, 64, 8, 2, 0, "bf16"), 4)
+        want = 256 + up(8 * T) + up(4 * T) + up(4 * nblk) + up(nblk * 3 * 512) + up(0) + up(0) \
+            + up(groups * 3 * 8 * 4) + up(groups * 8 * 1152 * 4)
+        assert got == want, (T, got, want)
