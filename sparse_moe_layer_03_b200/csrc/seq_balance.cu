@@ -16,7 +16,7 @@
 //   scores  logits, softmax, dl: reads x once.  Its logits are formed while count runs
 //   grads   dx and the partial sums of dWg: reads x again (from L2 where it fits), dx in and out
 //   finish  the partial sums of dWg and db in a fixed order, the losses
-// or, for 16-bit rows of 512 to 1152 and E <= 16, scores and grads as one kernel that reads x once (below;
+// or, for 16-bit rows of 640 to 1152 and E <= 16, scores and grads as one kernel that reads x once (below;
 // T = 32768, D = 1152, E = 8, dx added to: 48 us, 4.7 TB/s, against 23 + 43; the whole call 55 against 74).
 //
 // In the two kernels the mma.sync fragments are 16 consecutive bytes of a row in every lane.  Where an
@@ -721,12 +721,17 @@ __global__ void __launch_bounds__(128, NE == 4 ? 2 : 3) seq_grads_kernel(SeqBalA
 //   12 column warps, each a slice of 32-column groups over all the block's tokens: dWg in registers from
 //     the stage (transposed ldmatrix), dx from dl and the gate weight's columns in registers.
 // They meet on mbarriers only (dl full and empty by router, x full by stage); the last column warp to leave
-// a stage refills it.  For E <= 16 and rows of 512 (narrower ones leave the column warps too little: the two
+// a stage refills it.  For E <= 16 and rows of 640 (narrower ones leave the column warps too little: the two
 // kernels' many independent warps hide latency better) to 1152.
 constexpr int kFuRouters = 3, kFuCols = 12, kFuThreads = (kFuRouters + kFuCols) * 32;
 constexpr int kFuGroups = 3;                       // 32-column groups a column warp holds
-constexpr int kFuMinD = 512;                       // bf16, E = 8, T = 32768: 41.0 us against the two kernels' 39.6 at D = 512,
-                                                   // 45.1 against 52.4 at 768; 34.9 against 24.7 at 256
+// The narrowest row.  One kernel against two, bf16, E = 8, whole calls replayed from a graph (us): at T = 32768
+// 37.6 / 33.4 at D = 512, 39.4 / 35.8 at 576, 38.6 / 38.1 at 640, 40.0 / 41.1 at 704, 52.5 / 67.1 at 1152; at T = 8192
+// 18.3 / 18.3, 19.0 / 19.1, 18.6 / 19.8, 19.3 / 21.5, 22.4 / 27.5; at T = 512 10.9 / 11.2, 11.1 / 11.6, 11.3 / 12.0,
+// 11.4 / 12.4, 13.4 / 15.7.  Below 640 the two win by up to 4 us where calls are large, the one by up to 0.5
+// where they are small.  16 experts cross a little later (T = 32768: 46.1 / 43.7 at 640, 49.4 / 50.7 at 768), with
+// inputs out of L2 earlier (45.6 / 50.2 at 640, E = 8; 52.2 / 54.3, E = 16).
+constexpr int kFuMinD = 640;
 constexpr int kFuMaxStages = 6;
 constexpr int kFuMaxSmem = 232448;
 

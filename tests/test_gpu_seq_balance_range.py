@@ -60,6 +60,8 @@ def test_the_gate_row_of_a_rare_expert(T, D, E, low, dt):
     (333, 1152, 16, "race", [17, 333]),
     (14300, 512, 13, "race", [1, 14299]),
     (7200, 1152, 1, "topk", [40, 41, 7199]),
+    (8100, 640, 9, "topk", [19, 4000, 8090]),              # its narrowest rows
+    (7300, 640, 8, "race", [2, 7300]),
 ])
 def test_every_shape_of_the_one_kernel_form(T, D, E, routing, off, dt):
     if dt == "f32" and E * D > 51200:
