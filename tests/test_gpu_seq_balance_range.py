@@ -121,7 +121,7 @@ def test_a_layer_without_tokens(seq_len, offsets, routing):
 @pytest.mark.parametrize("T,D,E,routing,off", [
     (700, 256, 8, "topk", [0, 300, 612]), (333, 128, 16, "race", [17, 40, 333]), (400, 192, 24, "topk", [399, 400]),
     (5001, 768, 8, "topk", [9, 2000, 4991]), (2500, 1152, 16, "race", [5, 2000]), (5001, 128, 20, "topk", [33, 4000]),
-    (6000, 64, 4, "topk", [0, 3001]), (90, 64, 4, "topk", [7, 7]), (300, 512, 2, "topk", [300, 300])])
+    (6000, 64, 4, "topk", [0, 3001]), (90, 64, 4, "topk", [7, 7]), (300, 512, 2, "topk", [300, 300]), (100, 640, 4, "topk", [50])])
 def test_gates_of_every_row(T, D, E, routing, off, dt):
     c = Case(T, D, E, 2, dt, routing, off)
     held = []
