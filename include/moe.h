@@ -524,8 +524,8 @@ int moe_seq_balance(const moe_config_t* cfg, const void* x, const void* wg, cons
  * keeps the smallest code (4.4e-6 of its block's largest) at least, so that no first moment outlives
  * what it is divided by; on average an element that far below its largest moves by less than lr.
  * A block of 256 whose largest moment is below 2^-100 or not finite is stored as zeros; first
- * moments also where the second are not finite.  The denominator is at least 2^-126 (eps = 0 with
- * no gradient at all leaves a parameter as it is).
+ * moments also where the second are not finite.  The denominator is at least 2^-70, the gradient
+ * whose square leaves fp32's range (eps = 0 with no gradient at all leaves a parameter as it is).
  */
 typedef enum { MOE_MOMENTS_F32 = 0, MOE_MOMENTS_E4M3 = 1 } moe_moments_t;
 

@@ -266,7 +266,9 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // m, v and the root in the roundings of their formulas written out (no contraction, IEEE square
 // root): what is kept does not depend on how a compiler fuses them.  The update's quotient goes
 // through an approximate reciprocal (one unit in the last place): it is then scaled by lr and added
-// to a parameter some thousand times larger.  A denominator below 2^-126 counts as that.
+// to a parameter some thousand times larger.  A denominator below 2^-70 counts as that: the square of a
+// gradient below 8.4e-22, about 2^-70, times 1 - b2 = 0.001 is zero in fp32 (a root that is not is 2^-75 at
+// least), and with eps = 0 its first moment, which is not, would be divided by nothing.
 __device__ __forceinline__ float moments(float g, float& m, float& v, const StepScalars& s) {
   m = __fadd_rn(__fmul_rn(s.b1, m), __fmul_rn(s.omb1, g));
   v = __fadd_rn(__fmul_rn(s.b2, v), __fmul_rn(s.omb2, __fmul_rn(g, g)));
@@ -278,7 +280,7 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return r;
 }
 __device__ __forceinline__ float update(float p, float m, float root, float keep, const StepScalars& s) {
-  const float den = max_nan(fmaf(root, s.rs2, s.eps), 0x1p-126f);
+  const float den = max_nan(fmaf(root, s.rs2, s.eps), 0x1p-70f);
   return fmaf(-s.step_size, m * rcp_approx(den), __fmul_rn(p, keep));
 }
 
